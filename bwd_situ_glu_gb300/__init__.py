@@ -18,6 +18,8 @@ Binding names match the C entry points:
   forward in the GEMM's epilogue
 * ``situ_adam_update_host`` / ``situ_adam_stream_step``: Adam on host-resident state, the
   streamed form moving gradients and weights chunk by chunk
+* ``situ_route_topk``, ``situ_dispatch_plan``, ``situ_dispatch``, ``situ_combine``, ``situ_linear`` and their
+  gradients: the rest of the MoE layer (module ``moe``; C ABI ``include/situ_moe.h``)
 * ``situ_and_mul(x, beta, linear_beta)``: autograd function (forward kernel; backward kernel
   with p = 1), the pages' operator interface
 
@@ -39,11 +41,13 @@ INCLUDE = os.path.join(_ROOT, "include")
 LIB_DIR = os.path.join(_HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsitu_glu.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("situ_glu.cu", "situ_glu_fp8.cu", "situ_glu_dgrad.cu",
-                                             "situ_glu_gateup.cu", "situ_adam.cu", "situ_glu_selftest.cu")]
+                                             "situ_glu_gateup.cu", "situ_adam.cu", "situ_glu_selftest.cu", "situ_route.cu",
+                                             "situ_dispatch.cu", "situ_linear.cu", "situ_linear_bwd.cu")]
 # per-source extra flags: the host Adam update is a fixed sequence of IEEE fp32 operations
 SOURCE_FLAGS = {"situ_adam.cu": ["-Xcompiler", "-ffp-contract=off,-fno-fast-math,-fno-math-errno"]}
 DEPENDS = SOURCES + [os.path.join(CSRC, n) for n in ("situ_math.cuh", "situ_device.cuh", "situ_host.h",
-                                                     "situ_tc.cuh")] + [os.path.join(INCLUDE, "situ_glu.h")]
+                                                     "situ_tc.cuh", "situ_linear.cuh")] + [
+    os.path.join(INCLUDE, n) for n in ("situ_glu.h", "situ_moe.h")]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
@@ -146,6 +150,7 @@ def load():
     lib.situ_glu_last_cuda_error.restype = cint
     lib.situ_glu_version.argtypes = []
     lib.situ_glu_version.restype = cint
+    moe.declare(lib)
     _lib = lib
     return lib
 
@@ -505,11 +510,17 @@ def situ_adam_stream_step(grad, weight, master, m, v, params: AdamParams, stagin
                                             _stream_handle(stream, grad.device)))
 
 
+from . import moe  # noqa: E402  (the operators around the activation; uses the helpers above)
+from .moe import (situ_combine, situ_combine_bwd, situ_dispatch, situ_dispatch_plan, situ_linear,  # noqa: E402
+                  situ_linear_bwd, situ_route_topk, situ_route_topk_bwd)
+
 __all__ = [
     "build", "load", "version", "status_string", "SituGluError",
     "situ_glu_fwd", "situ_glu_bwd_router", "situ_glu_fwd_ptr", "situ_glu_bwd_router_ptr",
     "situ_glu_fwd_save_fp8", "situ_glu_bwd_router_fp8", "FP8_BLOCK", "fp8_scale_blocks",
     "situ_glu_bwd_router_dgrad", "situ_glu_bwd_router_dgrad_wd", "situ_glu_fwd_gateup",
     "situ_and_mul", "selftest_wait_timeout", "AdamParams", "adam_params", "situ_adam_update_host", "situ_adam_stream_step", "adam_staging_bytes",
+    "moe", "situ_route_topk", "situ_route_topk_bwd", "situ_dispatch_plan", "situ_dispatch", "situ_combine",
+    "situ_combine_bwd", "situ_linear", "situ_linear_bwd",
     "LIB_PATH", "INCLUDE",
 ]

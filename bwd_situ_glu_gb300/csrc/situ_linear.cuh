@@ -1,0 +1,56 @@
+// situ_linear.cuh — what the linear operator's forward and gradient kernels share: the activations and
+// their derivatives, and the prefix over experts.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/situ_moe.h"
+
+namespace situ_linear {
+
+constexpr uint32_t FULL_MASK = 0xffffffffu;
+
+// act(z) in fp32. silu: z·σ(z), with an exponential that overflows to +inf (z/inf = -0) below z ≈ -88.
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == SITU_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if constexpr (ACT == SITU_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+    if constexpr (ACT == SITU_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    return z;
+}
+
+// act'(z) in fp32.
+__device__ __forceinline__ float act_grad(int act, float z) {
+    switch (act) {
+        case SITU_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+        case SITU_ACT_SILU: {
+            const float s = 1.0f / (1.0f + __expf(-z));
+            return s * (1.0f + z * (1.0f - s));
+        }
+        case SITU_ACT_GELU:   // Φ(z) + z·φ(z)
+            return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+        default: return 1.0f;
+    }
+}
+
+// start[1 .. E] holds counts: their inclusive prefix in place, by one warp (each lane a segment).
+__device__ __forceinline__ void prefix_in_place(int* start, int E, int lane) {
+    const int seg = (E + 31) / 32;
+    const int b = 1 + lane * seg, en = min(E + 1, b + seg);
+    int sum = 0;
+    for (int i = b; i < en; ++i) sum += start[i];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL_MASK, incl, o);
+        if (lane >= o) incl += v;
+    }
+    int run = incl - sum;
+    for (int i = b; i < en; ++i) {
+        run += start[i];
+        start[i] = run;
+    }
+}
+
+}  // namespace situ_linear

@@ -1,0 +1,527 @@
+// situ_linear_bwd.cu — the linear operator's weight and bias gradients, and the step back through its
+// activation (include/situ_moe.h). The input gradient is a product like the forward: situ_linear.cu.
+//
+//   dz = dout·act'(z)                        elementwise, one pass over dout (and the saved z), which also
+//   db_e = Σ_{r in e} dz[r]                  sums the unrounded dz: HBM-bound
+//   dW_e = Σ_{r in e} dz[r]ᵀ·a[r]            a product per expert that contracts over its rows: tensor cores
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/situ_moe.h"
+#include "situ_device.cuh"
+#include "situ_host.h"
+#include "situ_linear.cuh"
+#include "situ_tc.cuh"
+
+namespace {
+
+using namespace situ;
+using namespace situ_host;
+using namespace situ_tc;
+using namespace situ_linear;
+
+// ---------------------------------------------------------------- dz and the bias gradient
+
+// Rows are cut into pieces of PIECE rows of one expert; a block takes a piece's 256 columns at a time
+// (8 per lane, its warps take rows in turn), adds its warps' sums in order and leaves them in
+// part[piece][column]; the second kernel adds an expert's pieces in order. No result depends on timing.
+constexpr int PIECE = 256;
+constexpr int BIAS_WARPS = 8;
+constexpr int BIAS_COLS = 256;
+
+int64_t max_pieces(int64_t R, int64_t E) { return R / PIECE + E; }
+
+template <bool DZ>
+__global__ void __launch_bounds__(BIAS_WARPS * 32)
+    act_bwd_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ pre, int act,
+                   const int64_t* __restrict__ offsets, uint16_t* __restrict__ dz, float* __restrict__ part, int E,
+                   int64_t R, int64_t N) {
+    __shared__ int start[MAX_EXPERTS + 1];
+    __shared__ float sums[BIAS_WARPS][BIAS_COLS + 8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int64_t b, en;
+        expert_range(offsets, e, R, b, en);
+        start[e + 1] = (int)((en - b + PIECE - 1) / PIECE);
+    }
+    if (threadIdx.x == 0) start[0] = 0;
+    __syncthreads();
+    if (warp == 0) prefix_in_place(start, E, lane);
+    __syncthreads();
+    const int64_t cb = (N + BIAS_COLS - 1) / BIAS_COLS, items = (int64_t)start[E] * cb;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int t = (int)(it / cb);
+        const int64_t col = (it - (int64_t)t * cb) * BIAS_COLS + lane * 8;
+        int lo = 0, hi = E - 1;              // last e with start[e] <= t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (start[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        int64_t b, en;
+        expert_range(offsets, lo, R, b, en);
+        const int64_t r0 = b + (int64_t)(t - start[lo]) * PIECE;
+        const int64_t r1 = min(en, r0 + PIECE);
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+        if (col < N) {                       // N % 8 == 0: whole vectors
+#pragma unroll 4
+            for (int64_t r = r0 + warp; r < r1; r += BIAS_WARPS) {
+                const Vec<4> g = ld_stream<4, true>((const Vec<4>*)(dout + r * N + col));
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[2 * i] = bf16_lo(g.w[i]);
+                    f[2 * i + 1] = bf16_hi(g.w[i]);
+                }
+                if constexpr (DZ) {
+                    const Vec<4> z = ld_stream<4, true>((const Vec<4>*)(pre + r * N + col));
+                    Vec<4> o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[2 * i] *= act_grad(act, bf16_lo(z.w[i]));
+                        f[2 * i + 1] *= act_grad(act, bf16_hi(z.w[i]));
+                        o.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+                    }
+                    st_stream<4>((Vec<4>*)(dz + r * N + col), o);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] += f[i];
+            }
+        }
+        if (part) {                          // uniform over the grid
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = s[i];
+            __syncthreads();
+            const int64_t c = (it - (int64_t)t * cb) * BIAS_COLS + threadIdx.x;
+            if (c < N) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < BIAS_WARPS; ++w) v += sums[w][threadIdx.x];
+                part[(int64_t)t * N + c] = v;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// blockIdx.y: expert; blockIdx.x: 256 columns.
+__global__ void __launch_bounds__(BIAS_COLS)
+    bias_sum_kernel(const float* __restrict__ part, const int64_t* __restrict__ offsets, float* __restrict__ dbias,
+                    int64_t R, int64_t N) {
+    const int e = blockIdx.y, lane = threadIdx.x & 31;
+    __shared__ int s_first[BIAS_COLS / 32];
+    int first = 0;                           // pieces of the experts before e
+    for (int i = threadIdx.x; i < e; i += blockDim.x) {
+        int64_t b, en;
+        expert_range(offsets, i, R, b, en);
+        first += (int)((en - b + PIECE - 1) / PIECE);
+    }
+    first = (int)__reduce_add_sync(FULL_MASK, (unsigned)first);
+    if (lane == 0) s_first[threadIdx.x >> 5] = first;
+    __syncthreads();
+    first = 0;
+#pragma unroll
+    for (int i = 0; i < BIAS_COLS / 32; ++i) first += s_first[i];
+    int64_t b, en;
+    expert_range(offsets, e, R, b, en);
+    const int64_t n = (en - b + PIECE - 1) / PIECE;
+    const int64_t c = (int64_t)blockIdx.x * BIAS_COLS + threadIdx.x;
+    if (c >= N) return;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int64_t i = 0; i < n; ++i) v += part[(first + i) * N + c];
+    dbias[(int64_t)e * N + c] = v;
+}
+
+// ---------------------------------------------------------------- the weight gradient
+
+// dW_e [N, K] = dz_eᵀ·a_e on the tensor cores. A job is a 128 x 256 tile of one expert's dW; its
+// contraction runs over the expert's rows, 64 to a ring stage. Both operands are read as they are
+// stored, rows apart ("MN-major": per stage two 64-column boxes of dz, four of a, 128-byte swizzle).
+// A TMA box cannot end at an expert's last row, so the last stage brings rows of the next expert (or
+// zeros past the tensor): the MMA warp issues only the 16-row steps that hold rows of the expert and
+// first zeroes, in both operands, the rows past its end in the last step (generic-proxy writes, then
+// the proxy fence), so nothing of another expert enters, NaN included.
+//
+// The tensor cores cut each step's fp32 sum towards zero, an error that grows with the steps (measured
+// against float64 at 2048 x 2048: 5e-7 of the norm after 512 rows, 4.4e-6 after 4096, 1.9e-5 after
+// 16384). dW feeds an fp32 optimizer, so an accumulator takes at most CHUNK_BLOCKS stages (512 rows)
+// and the epilogue's threads add the chunks in registers, rounded to nearest, while the tensor cores
+// fill the other accumulator. Where the tiles of dW cannot
+// fill the SMs, the rows are cut into `splits` pieces whose sums (fp32, in the workspace) a second
+// kernel adds in order.
+constexpr int CHUNK_BLOCKS = 8;
+constexpr int EPW = 2;
+constexpr int NUM_EPI_THREADS = 4 * EPW * 32;
+constexpr int NUM_THREADS = 64 + NUM_EPI_THREADS;
+constexpr int STAGE_TILE = 32 * 128;         // 32 rows x 128 bytes of dW
+constexpr int BOX_BYTES = 64 * BK * 2;       // 64 columns x 64 rows
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 4 * EPW * STAGE_TILE + (int)sizeof(Barriers);
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+
+struct WJob {
+    int e, mt, nt, plane;
+    int64_t row0, rows;                      // rows to contract over
+};
+
+__device__ __forceinline__ WJob wgrad_job(int64_t j, const int64_t* offsets, int E, int64_t R, int MT, int NT,
+                                          int splits) {
+    WJob w;
+    w.nt = (int)(j % NT);
+    j /= NT;
+    w.mt = (int)(j % MT);
+    j /= MT;
+    const int s = (int)(j % splits);
+    w.e = (int)(j / splits);
+    w.plane = s * E + w.e;
+    int64_t b, en;
+    expert_range(offsets, w.e, R, b, en);
+    const int64_t blocks = (en - b + BK - 1) / BK, per = (blocks + splits - 1) / splits;
+    w.row0 = min(en, b + s * per * BK);
+    w.rows = min(en, w.row0 + per * BK) - w.row0;
+    return w;
+}
+
+// OUT_FP32: dW (or a partial sum) in fp32, else bf16.
+template <bool OUT_FP32>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    wgrad_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_a,
+                 const __grid_constant__ CUtensorMap map_dw, const int64_t* __restrict__ offsets,
+                 int* __restrict__ status, int E, int64_t R, int64_t N, int64_t K, int MT, int NT, int splits) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* staging = ring + STAGES * STAGE_BYTES;
+    Barriers* bars = (Barriers*)(staging + 4 * EPW * STAGE_TILE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t jobs = (int64_t)E * splits * MT * NT;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&bars->tfull[a], 1);
+            mbar_init(&bars->tempty[a], NUM_EPI_THREADS);
+        }
+        mbar_init(&bars->mma_done, 1);
+        bars->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars->tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, pending = 0, pend_par = 0;
+            const uint64_t pol = make_policy<L2Hint::normal>();
+            bool ok = true;
+            for (int64_t j = blockIdx.x; ok && j < jobs; j += gridDim.x) {
+                const WJob w = wgrad_job(j, offsets, E, R, MT, NT, splits);
+                const int kbs = (int)((w.rows + BK - 1) / BK);
+                for (int kb = 0; kb < kbs; ++kb) {
+                    if (!mbar_wait(&bars->empty[stage], phase ^ 1, bars, status)) { ok = false; break; }
+                    mbar_expect_tx(&bars->full[stage], STAGE_BYTES);
+                    uint8_t* sa = ring + stage * STAGE_BYTES;
+                    const int row = (int)(w.row0 + (int64_t)kb * BK);
+#pragma unroll
+                    for (int i = 0; i < BM / 64; ++i)
+                        tma_load_2d_hint(sa + i * BOX_BYTES, &map_dz, w.mt * BM + 64 * i, row, &bars->full[stage], pol);
+#pragma unroll
+                    for (int i = 0; i < BN / 64; ++i)
+                        tma_load_2d_hint(sa + A_BYTES + i * BOX_BYTES, &map_a, w.nt * BN + 64 * i, row, &bars->full[stage], pol);
+                    pending |= 1u << stage;
+                    pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+            }
+            for (int s = 0; s < STAGES; ++s)
+                if (pending & (1u << s)) mbar_drain(&bars->full[s], (pend_par >> s) & 1u);
+        }
+    } else if (warp == 1) {
+        // the whole warp walks the stages (it zeroes the rows past an expert's end); lane 0 issues
+        int stage = 0, done = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t j = blockIdx.x; ok && j < jobs; j += gridDim.x) {
+            const WJob w = wgrad_job(j, offsets, E, R, MT, NT, splits);
+            const int kbs = (int)((w.rows + BK - 1) / BK);
+            for (int kb = 0; ok && kb < kbs; ++kb) {
+                const int acc = done & 1, in_chunk = kb % CHUNK_BLOCKS;
+                const bool chunk_ends = in_chunk + 1 == CHUNK_BLOCKS || kb + 1 == kbs;
+                const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
+                if (in_chunk == 0) {
+                    ok = __all_sync(FULL_MASK, mbar_wait(&bars->tempty[acc], (uint32_t)((done >> 1) & 1) ^ 1, bars, status));
+                    if (!ok) break;
+                }
+                ok = __all_sync(FULL_MASK, mbar_wait(&bars->full[stage], phase, bars, status));
+                if (!ok) break;
+                uint8_t* sa = ring + stage * STAGE_BYTES;
+                const int valid = (int)min((int64_t)BK, w.rows - (int64_t)kb * BK);
+                const int steps = (valid + UK - 1) / UK;
+                if (valid < steps * UK) {
+                    const int n16 = (steps * UK - valid) * 8;          // 16-byte pieces per box
+                    for (int i = lane; i < n16 * (STAGE_BYTES / BOX_BYTES); i += 32) {
+                        const int box = i / n16;
+                        st_shared_v4(sa + box * BOX_BYTES + valid * 128 + (i - box * n16) * 16, 0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t ad = smem_desc_mn(smem_addr(sa)), bd = smem_desc_mn(smem_addr(sa + A_BYTES));
+                    for (int kk = 0; kk < steps; ++kk)   // 16 rows = 2048 bytes further (128 descriptor units)
+                        tc_mma_abmn(d_tmem, ad + (uint64_t)(kk * 128), bd + (uint64_t)(kk * 128), (in_chunk > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(&bars->empty[stage]);
+                    if (chunk_ends) tc_commit(&bars->tfull[acc]);
+                }
+                __syncwarp();
+                done += chunk_ends;
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
+            }
+        }
+        if (lane == 0) {
+            tc_commit(&bars->mma_done);
+            mbar_drain(&bars->mma_done, 0);
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3;
+        const int slot = (warp - 2) >> 2;
+        const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
+        uint8_t* stage = staging + (warp - 2) * STAGE_TILE;
+        constexpr int COLS = BN / EPW;               // columns of this warp
+        constexpr int CW = OUT_FP32 ? 32 : 64;       // columns per 128-byte staged row
+        bool stores_pending = false;
+        bool ok = true;
+        int done = 0;
+        for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
+            const WJob w = wgrad_job(j, offsets, E, R, MT, NT, splits);
+            const int chunks = (int)((w.rows + CHUNK_BLOCKS * BK - 1) / (CHUNK_BLOCKS * BK));
+            float sum[COLS];
+#pragma unroll
+            for (int i = 0; i < COLS; ++i) sum[i] = 0.0f;
+            for (int ch = 0; ch < chunks; ++ch, ++done) {
+                const int acc = done & 1;
+                if (ok && !mbar_wait(&bars->tfull[acc], (uint32_t)((done >> 1) & 1), bars, status)) ok = false;
+                ok = __all_sync(FULL_MASK, ok);
+                tc_fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int h = 0; h < COLS; h += 32) {
+                        float v[32];
+                        tc_ld<32>(tmem + t_lane + (uint32_t)(acc * BN + slot * COLS + h), v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[h + i] += v[i];
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&bars->tempty[acc]);
+            }
+            const int n0 = w.mt * BM + quad * 32;
+#pragma unroll
+            for (int c = 0; c < COLS; c += CW) {
+                const int col = w.nt * BN + slot * COLS + c;
+                if (!ok || n0 >= N || col >= K) continue;      // uniform over the warp
+                if (stores_pending) {
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint8_t* at = stage + lane * 128 + ((q ^ (lane & 7)) << 4);
+                    if constexpr (OUT_FP32) {
+                        st_shared_v4(at, __float_as_uint(sum[c + 4 * q]), __float_as_uint(sum[c + 4 * q + 1]),
+                                     __float_as_uint(sum[c + 4 * q + 2]), __float_as_uint(sum[c + 4 * q + 3]));
+                    } else {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[i] = pack_bf16x2(sum[c + 8 * q + 2 * i], sum[c + 8 * q + 2 * i + 1]);
+                        st_shared_v4(at, p[0], p[1], p[2], p[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&map_dw, col, n0, w.plane, stage);
+                    bulk_commit();
+                }
+                stores_pending = true;
+            }
+        }
+        if (lane == 0 && stores_pending) bulk_wait_all();
+    }
+    pipeline_teardown(tmem);
+}
+
+// dw = the sum of `splits` partial sums of n elements each, in order.
+template <bool OUT_FP32>
+__global__ void __launch_bounds__(256)
+    wgrad_sum_kernel(const float* __restrict__ part, void* __restrict__ dw, int64_t n, int splits) {
+    for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * blockDim.x * 4) {
+        float4 s = *(const float4*)(part + i);           // n % 4 == 0
+        for (int k = 1; k < splits; ++k) {
+            const float4 v = *(const float4*)(part + k * n + i);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        if constexpr (OUT_FP32) *(float4*)((float*)dw + i) = s;
+        else *(uint2*)((uint16_t*)dw + i) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+}
+
+constexpr int64_t MAX_SPLITS = 16;
+constexpr int64_t SPLIT_MIN_ROWS = 256;      // a piece of fewer rows does not pay for its partial sum
+constexpr int SM_COUNT = 152;                // what the workspace is sized for: the split must not need a device
+
+// Pieces of the contraction: as many as fill the SMs with jobs.
+int64_t wgrad_splits(int64_t R, int64_t N, int64_t K, int64_t E) {
+    const int64_t jobs = E * ((N + BM - 1) / BM) * ((K + BN - 1) / BN);
+    int64_t s = SM_COUNT / jobs;
+    const int64_t most = R / E / SPLIT_MIN_ROWS;
+    if (s > most) s = most;
+    if (s > MAX_SPLITS) s = MAX_SPLITS;
+    return s < 1 ? 1 : s;
+}
+
+int check_linear(int64_t E, const void* offsets, int64_t R, int64_t N, int64_t K) {
+    if (R < 0 || R > INT32_MAX || N < 8 || N % 8 != 0 || K < 8 || K % 8 != 0 || E < 1 || E > MAX_EXPERTS)
+        return SITU_GLU_INVALID_ARG;
+    if (N > INT32_MAX / 4 || K > INT32_MAX / 4 || E * N > INT32_MAX || E * K > INT32_MAX) return SITU_GLU_INVALID_ARG;
+    if (!offsets && E != 1) return SITU_GLU_INVALID_ARG;
+    return SITU_GLU_OK;
+}
+
+int sm_count(int* sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t situ_linear_act_bwd_workspace(int64_t R, int64_t N, int64_t E) {
+    if (check_linear(E, (const void*)8, R, N, 8) != SITU_GLU_OK) return 0;
+    return max_pieces(R, E) * N * 4;
+}
+
+int situ_linear_act_bwd(const void* dout, const void* pre, int act, const int64_t* expert_offsets, int64_t E, void* dz,
+                        float* dbias, void* workspace, int64_t workspace_bytes, int64_t R, int64_t N,
+                        cudaStream_t stream) {
+    int st = check_linear(E, expert_offsets, R, N, 8);
+    if (st != SITU_GLU_OK) return st;
+    if (act < SITU_ACT_NONE || act > SITU_ACT_GELU) return SITU_GLU_INVALID_ARG;
+    const bool with_dz = act != SITU_ACT_NONE;
+    const int64_t need = dbias ? situ_linear_act_bwd_workspace(R, N, E) : 0;
+    if (R > 0 && (!dout || (with_dz && (!pre || !dz)))) return SITU_GLU_INVALID_ARG;
+    if (dbias && (workspace_bytes < need || !workspace)) return SITU_GLU_INVALID_ARG;
+    if (!aligned(dout, 16) || !aligned(pre, 16) || !aligned(dz, 16) || !aligned(dbias, 4) || !aligned(workspace, 4) ||
+        !aligned(expert_offsets, 8))
+        return SITU_GLU_INVALID_ARG;
+    const Range in[3] = {range_of(dout, R * N * 2), range_of(pre, with_dz ? R * N * 2 : 0),
+                         range_of(expert_offsets, expert_offsets ? (E + 1) * 8 : 0)};
+    const Range o[3] = {range_of(dz, with_dz ? R * N * 2 : 0), range_of(dbias, dbias ? E * N * 4 : 0),
+                        range_of(workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (overlap(o[i], r)) return SITU_GLU_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (overlap(o[i], o[j])) return SITU_GLU_OVERLAP;
+    }
+    if (R > 0 && (with_dz || dbias)) {
+        auto kernel = with_dz ? act_bwd_kernel<true> : act_bwd_kernel<false>;
+        int grid = 0;
+        const int64_t items = max_pieces(R, E) * ((N + BIAS_COLS - 1) / BIAS_COLS);
+        st = grid_for((const void*)kernel, BIAS_WARPS * 32, items * BIAS_WARPS, &grid);
+        if (st != SITU_GLU_OK) return st;
+        kernel<<<grid, BIAS_WARPS * 32, 0, stream>>>((const uint16_t*)dout, (const uint16_t*)pre, act, expert_offsets,
+                                                     (uint16_t*)dz, dbias ? (float*)workspace : nullptr, (int)E, R, N);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    if (dbias) {
+        bias_sum_kernel<<<dim3((unsigned)((N + BIAS_COLS - 1) / BIAS_COLS), (unsigned)E), BIAS_COLS, 0, stream>>>(
+            (const float*)workspace, expert_offsets, dbias, R, N);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return SITU_GLU_OK;
+}
+
+int64_t situ_linear_wgrad_workspace(int64_t R, int64_t N, int64_t K, int64_t E) {
+    if (check_linear(E, (const void*)8, R, N, K) != SITU_GLU_OK) return 0;
+    const int64_t s = wgrad_splits(R, N, K, E);
+    return s > 1 ? s * E * N * K * 4 : 0;
+}
+
+int situ_linear_wgrad(const void* dz, const void* a, const int64_t* expert_offsets, int64_t E, void* dw, int dw_type,
+                      void* workspace, int64_t workspace_bytes, int* status, int64_t R, int64_t N, int64_t K,
+                      cudaStream_t stream) {
+    int st = check_linear(E, expert_offsets, R, N, K);
+    if (st != SITU_GLU_OK) return st;
+    if (dw_type != SITU_BF16 && dw_type != SITU_FP32) return SITU_GLU_INVALID_ARG;
+    const int64_t need = situ_linear_wgrad_workspace(R, N, K, E);
+    if (!dw || (R > 0 && (!dz || !a)) || workspace_bytes < need || (need && !workspace)) return SITU_GLU_INVALID_ARG;
+    if (!aligned(dz, 16) || !aligned(a, 16) || !aligned(dw, 16) || !aligned(workspace, 16) ||
+        !aligned(expert_offsets, 8) || !aligned(status, 4))
+        return SITU_GLU_INVALID_ARG;
+    const int64_t dw_bytes = E * N * K * (dw_type == SITU_FP32 ? 4 : 2);
+    const Range in[3] = {range_of(dz, R * N * 2), range_of(a, R * K * 2),
+                         range_of(expert_offsets, expert_offsets ? (E + 1) * 8 : 0)};
+    const Range o[3] = {range_of(dw, dw_bytes), range_of(workspace, need), range_of(status, status ? 4 : 0)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (overlap(o[i], r)) return SITU_GLU_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (overlap(o[i], o[j])) return SITU_GLU_OVERLAP;
+    }
+    if (R == 0) {
+        const cudaError_t e = cudaMemsetAsync(dw, 0, (size_t)dw_bytes, stream);
+        return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
+    }
+    const int64_t splits = wgrad_splits(R, N, K, E);
+    const bool fp32 = splits > 1 || dw_type == SITU_FP32;
+    const int MT = (int)((N + BM - 1) / BM), NT = (int)((K + BN - 1) / BN);
+    CUtensorMap map_dz, map_a, map_dw;
+    if (!make_map(&map_dz, dz, (uint64_t)R, (uint64_t)N, BK) || !make_map(&map_a, a, (uint64_t)R, (uint64_t)K, BK))
+        return cuda_fail(cudaErrorInvalidValue);
+    const uint64_t sz = fp32 ? 4 : 2;
+    const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)(E * splits)};
+    const uint64_t strides[2] = {(uint64_t)K * sz, (uint64_t)K * (uint64_t)N * sz};
+    const uint32_t box[3] = {(uint32_t)(128 / sz), 32, 1};
+    if (!make_map_any(&map_dw, splits > 1 ? workspace : dw, fp32, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cuda_fail(cudaErrorInvalidValue);
+    auto kernel = fp32 ? wgrad_kernel<true> : wgrad_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return cuda_fail(e);
+    int sms = 0;
+    if ((st = sm_count(&sms)) != SITU_GLU_OK) return st;
+    const int64_t jobs = E * splits * MT * NT;
+    kernel<<<(unsigned)(jobs < sms ? jobs : sms), NUM_THREADS, SMEM_BYTES, stream>>>(
+        map_dz, map_a, map_dw, expert_offsets, status, (int)E, R, N, K, MT, NT, (int)splits);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+    if (splits > 1) {
+        const int64_t n = E * N * K, blocks = (n / 4 + 255) / 256;
+        const unsigned grid = (unsigned)(blocks < sms * 8 ? blocks : sms * 8);
+        if (dw_type == SITU_FP32) wgrad_sum_kernel<true><<<grid, 256, 0, stream>>>((const float*)workspace, dw, n, (int)splits);
+        else wgrad_sum_kernel<false><<<grid, 256, 0, stream>>>((const float*)workspace, dw, n, (int)splits);
+        if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+    }
+    return SITU_GLU_OK;
+}
+
+}  // extern "C"

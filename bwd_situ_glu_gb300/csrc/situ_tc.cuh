@@ -187,6 +187,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c0, int c1, int c2, const void* src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0),
+                 "r"(c1), "r"(c2), "r"(smem_addr(src))
+                 : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Wait until the committed bulk stores of this thread have finished reading shared memory.
@@ -246,6 +252,17 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(B_MN ? IDESC_BMN : IDESC), "r"(accumulate)
+        : "memory");
+}
+
+// The same with both operands MN-major ("transpose A" is bit 15): the weight gradient contracts over
+// rows, along which neither operand is contiguous.
+constexpr uint32_t IDESC_ABMN = IDESC | (1u << 15) | (1u << 16);
+__device__ __forceinline__ void tc_mma_abmn(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(IDESC_ABMN), "r"(accumulate)
         : "memory");
 }
 
@@ -358,8 +375,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* b, uint32_t parity, 
 __device__ __forceinline__ void epi_barrier(int nthreads) { asm volatile("bar.sync 1, %0;" ::"r"(nthreads) : "memory"); }
 
 // Expert e's rows as [begin, end) clamped into [0, R] (end >= begin): malformed offsets can
-// neither index outside the row range nor inflate the number of tiles beyond R/BM + E.
+// neither index outside the row range nor inflate the number of tiles beyond R/BM + E. Without
+// offsets (the dense products) the one expert owns every row.
 __device__ __forceinline__ void expert_range(const int64_t* off, int e, int64_t R, int64_t& begin, int64_t& end) {
+    if (!off) {
+        begin = 0;
+        end = R;
+        return;
+    }
     int64_t a = off[e], b = off[e + 1];
     a = a < 0 ? 0 : (a > R ? R : a);
     b = b < a ? a : (b > R ? R : b);
@@ -696,6 +719,26 @@ inline bool make_map_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t 
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A tensor map of any of the shapes above with its own swizzle and element type: rank 2 or 3, dims
+// innermost first, strides in bytes of dims 1 .. rank - 1. Reads past the end are zeros, writes past
+// the end are dropped.
+inline bool make_map_any(CUtensorMap* m, const void* base, bool fp32, int rank, const uint64_t* dims,
+                         const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                         CUtensorMapL2promotion promo = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+    EncodeTiled fn = encode_fn();
+    if (!fn || rank < 2 || rank > 3) return false;
+    cuuint64_t d[3], st[2];
+    cuuint32_t b[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+              const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promo,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -1,0 +1,462 @@
+"""The operators around the expert activation in one MoE layer (C ABI: ``include/situ_moe.h``).
+
+* ``situ_route_topk`` / ``situ_route_topk_bwd``: top-k softmax of the router scores
+* ``situ_dispatch_plan``: the token-expert pairs in expert order (offsets, rows and back)
+* ``situ_dispatch``: tokens copied to their rows (its gradient is ``situ_combine`` without weights)
+* ``situ_combine`` / ``situ_combine_bwd``: the weighted rows of a token summed back
+* ``situ_linear`` / ``situ_linear_bwd``: per-expert or dense product with bias, activation, residual
+* ``route_topk``, ``moe_dispatch``, ``moe_combine``, ``linear``: the same as autograd operators
+
+Like the rest of the package these check tensor metadata, marshal pointers and raise ``SituGluError``
+on a non-zero status; every tensor is contiguous and on one CUDA device. ``stream`` (a torch stream or
+a raw handle; default: the current stream) is where the work runs; outputs that are not given and
+workspaces are allocated on that stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from contextlib import contextmanager
+
+import bwd_situ_glu_gb300 as _sg
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+MAX_EXPERTS, MAX_TOPK = 1024, 32  # SITU_MAX_EXPERTS, SITU_MAX_TOPK
+
+
+def declare(lib):
+    """ctypes signatures of include/situ_moe.h (called once by load())."""
+    vp, i64, cint = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    for name, args, ret in (
+            ("situ_route_topk", [vp, cint, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_route_topk_bwd", [vp, vp, vp, vp, i64, vp, cint, i64, i64, i64, vp], cint),
+            ("situ_dispatch_plan_workspace", [i64, i64, i64], i64),
+            ("situ_dispatch_plan", [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_dispatch", [vp, cint, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_combine", [vp, cint, vp, vp, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_combine_bwd", [vp, vp, cint, vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_linear_fwd", [vp, vp, vp, i64, vp, vp, cint, vp, cint, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_linear_act_bwd_workspace", [i64, i64, i64], i64),
+            ("situ_linear_act_bwd", [vp, vp, cint, vp, i64, vp, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_linear_dgrad", [vp, vp, vp, i64, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_linear_wgrad_workspace", [i64, i64, i64, i64], i64),
+            ("situ_linear_wgrad", [vp, vp, vp, i64, vp, cint, vp, i64, vp, i64, i64, i64, vp], cint)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ret
+
+
+def _type(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _one_device(*tensors):
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("all tensors must be on the same device")
+
+
+@contextmanager
+def _other_stream(stream, device):
+    import torch
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield int(stream.cuda_stream)
+
+
+@contextmanager
+def _other_device(device):
+    import torch
+    with torch.cuda.device(device):
+        yield int(torch.cuda.current_stream(device).cuda_stream)
+
+
+class _Here:
+    """The current stream of the current device: nothing to switch."""
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _launch(stream, device):
+    """Context in which allocations belong to the launch stream; gives its handle."""
+    import torch
+    if stream is not None:
+        return _other_stream(stream, device)
+    if device.index == torch.cuda.current_device():
+        return _Here(torch.cuda.current_stream(device).cuda_stream)
+    return _other_device(device)
+
+
+def _out(t, shape, dtype, like, name):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _sg._need(t, dtype, shape, name)
+    return t
+
+
+def _scratch(nbytes, like):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+
+
+# ---------------------------------------------------------------- routing
+
+def situ_route_topk(logits, k, p=None, ids=None, stream=None):
+    """(p fp32 [T,k], ids int32 [T,k]): softmax over the k largest scores of each token, in descending
+    order, ties to the lower index. A score of -inf is never chosen (id -1, p 0). logits [T,E] bf16 or
+    fp32, E <= 1024, k <= min(E, 32)."""
+    import torch
+    ty = _type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    _sg._need(logits, logits.dtype, (T, E), "logits")
+    with _launch(stream, logits.device) as s:
+        p = _out(p, (T, k), torch.float32, logits, "p")
+        ids = _out(ids, (T, k), torch.int32, logits, "ids")
+        _one_device(logits, p, ids)
+        _sg._check(_sg.load().situ_route_topk(logits.data_ptr(), ty, p.data_ptr(), ids.data_ptr(), T, E, k, s))
+    return p, ids
+
+
+def situ_route_topk_bwd(ids, p, dp, num_experts, dtype=None, row_of=None, dlogits=None, stream=None):
+    """dlogits [T,num_experts] of ``dtype`` (default fp32): p_k(dp_k - sum_j p_j dp_j) at ids, 0 elsewhere.
+    dp fp32 [T,k], or with ``row_of`` (int32 [T,k]) fp32 [R] in row order."""
+    import torch
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    T, k = ids.shape
+    _sg._need(ids, torch.int32, (T, k), "ids")
+    _sg._need(p, torch.float32, (T, k), "p")
+    R = 0
+    if row_of is None:
+        _sg._need(dp, torch.float32, (T, k), "dp")
+    else:
+        _sg._need(row_of, torch.int32, (T, k), "row_of")
+        R = dp.numel()
+        _sg._need(dp, torch.float32, (R,), "dp")
+    if dlogits is not None:
+        dtype = dlogits.dtype
+    with _launch(stream, ids.device) as s:
+        dlogits = _out(dlogits, (T, num_experts), dtype or torch.float32, ids, "dlogits")
+        _one_device(ids, p, dp, row_of, dlogits)
+        _sg._check(_sg.load().situ_route_topk_bwd(ids.data_ptr(), p.data_ptr(), dp.data_ptr(), _ptr(row_of), R,
+                                                  dlogits.data_ptr(), _type(dlogits, "dlogits"), T, num_experts, k, s))
+    return dlogits
+
+
+# ---------------------------------------------------------------- tokens sorted by expert and back
+
+def situ_dispatch_plan(ids, num_experts, p=None, stream=None):
+    """(expert_offsets int64 [E+1], row_of int32 [T,k], src int32 [T*k], p_rows fp32 [T*k] or None): the rows
+    of the token-expert pairs, sorted by expert and, within one, by token and choice. An id outside
+    [0, num_experts) has no row (row_of -1); src past the last row is -1, p_rows 0."""
+    import torch
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    T, k = ids.shape
+    _sg._need(ids, torch.int32, (T, k), "ids")
+    if p is not None:
+        _sg._need(p, torch.float32, (T, k), "p")
+        _one_device(ids, p)
+    lib = _sg.load()
+    with _launch(stream, ids.device) as s:
+        new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=ids.device)  # noqa: E731
+        offsets = new(num_experts + 1 if num_experts > 0 else 0, dtype=torch.int64)
+        row_of, src = new(T, k), new(T * k)
+        p_rows = None if p is None else new(T * k, dtype=torch.float32)
+        nb = lib.situ_dispatch_plan_workspace(T, k, num_experts)
+        ws = _scratch(nb, ids)
+        # without tokens there is nothing to weigh: the pointers of empty tensors are null
+        _sg._check(lib.situ_dispatch_plan(ids.data_ptr(), _ptr(p), offsets.data_ptr(), row_of.data_ptr(),
+                                          src.data_ptr(), _ptr(p_rows), _ptr(ws), nb, T, k, num_experts, s))
+    return offsets, row_of, src, p_rows
+
+
+def situ_dispatch(x, row_of, expert_offsets, weights=None, h=None, stream=None):
+    """h [T*k, D]: h[row_of[t,j]] = x[t], or weights[t,j]*x[t] with weights fp32 [T,k]; rows that belong to no
+    token are zero. x [T,D] bf16 or fp32."""
+    import torch
+    ty = _type(x, "x")
+    if x.dim() != 2 or row_of.dim() != 2:
+        raise ValueError("x must be [T, D] and row_of [T, k]")
+    (T, D), k = x.shape, row_of.shape[1]
+    _sg._need(x, x.dtype, (T, D), "x")
+    _sg._need(row_of, torch.int32, (T, k), "row_of")
+    E = expert_offsets.numel() - 1
+    _sg._need(expert_offsets, torch.int64, (E + 1,), "expert_offsets")
+    if weights is not None:
+        _sg._need(weights, torch.float32, (T, k), "weights")
+    with _launch(stream, x.device) as s:
+        h = _out(h, (T * k, D), x.dtype, x, "h")
+        _one_device(x, row_of, expert_offsets, weights, h)
+        _sg._check(_sg.load().situ_dispatch(x.data_ptr(), ty, row_of.data_ptr(), expert_offsets.data_ptr(), E,
+                                            _ptr(weights), h.data_ptr(), T, k, T * k, D, s))
+    return h
+
+
+def situ_combine(o, row_of, weights=None, residual=None, y=None, stream=None):
+    """y [T,D] = residual + sum_j weights[t,j]*o[row_of[t,j]] (weights default to 1, residual to 0; fp32,
+    rounded once). o [R,D] bf16 or fp32; ``y`` may be ``residual`` itself."""
+    import torch
+    ty = _type(o, "o")
+    if o.dim() != 2 or row_of.dim() != 2:
+        raise ValueError("o must be [R, D] and row_of [T, k]")
+    (R, D), (T, k) = o.shape, row_of.shape
+    _sg._need(o, o.dtype, (R, D), "o")
+    _sg._need(row_of, torch.int32, (T, k), "row_of")
+    if weights is not None:
+        _sg._need(weights, torch.float32, (T, k), "weights")
+    if residual is not None:
+        _sg._need(residual, o.dtype, (T, D), "residual")
+    with _launch(stream, o.device) as s:
+        y = _out(y, (T, D), o.dtype, o, "y")
+        _one_device(o, row_of, weights, residual, y)
+        _sg._check(_sg.load().situ_combine(o.data_ptr(), ty, row_of.data_ptr(), _ptr(weights), _ptr(residual),
+                                           y.data_ptr(), T, k, R, D, s))
+    return y
+
+
+def situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do=None, dweights=None, stream=None):
+    """(do [R,D] of o's type, dweights fp32 [T,k]): do[row_of[t,j]] = weights[t,j]*dy[t] (rows of no token are
+    zero), dweights[t,j] = <dy[t], o[row_of[t,j]]> (0 without a row)."""
+    import torch
+    ty = _type(o, "o")
+    if o.dim() != 2 or row_of.dim() != 2:
+        raise ValueError("o must be [R, D] and row_of [T, k]")
+    (R, D), (T, k) = o.shape, row_of.shape
+    _sg._need(o, o.dtype, (R, D), "o")
+    _sg._need(dy, o.dtype, (T, D), "dy")
+    _sg._need(row_of, torch.int32, (T, k), "row_of")
+    _sg._need(weights, torch.float32, (T, k), "weights")
+    E = expert_offsets.numel() - 1
+    _sg._need(expert_offsets, torch.int64, (E + 1,), "expert_offsets")
+    with _launch(stream, o.device) as s:
+        do = _out(do, (R, D), o.dtype, o, "do")
+        dweights = _out(dweights, (T, k), torch.float32, o, "dweights")
+        _one_device(dy, o, row_of, weights, expert_offsets, do, dweights)
+        _sg._check(_sg.load().situ_combine_bwd(dy.data_ptr(), o.data_ptr(), ty, row_of.data_ptr(), weights.data_ptr(),
+                                               expert_offsets.data_ptr(), E, do.data_ptr(), dweights.data_ptr(), T, k,
+                                               R, D, s))
+    return do, dweights
+
+
+# ---------------------------------------------------------------- linear
+
+def _linear_shape(a, w, expert_offsets, a_name="a"):
+    """(R, N, K, E, lead): w is [N,K] without expert_offsets, [E,N,K] with them; lead is () or (E,)."""
+    import torch
+    if a.dim() != 2:
+        raise ValueError(f"{a_name} must be two-dimensional")
+    if expert_offsets is None:
+        if w.dim() != 2:
+            raise ValueError("w must be [N, K] without expert_offsets")
+        E, lead = 1, ()
+    else:
+        if w.dim() != 3:
+            raise ValueError("w must be [E, N, K] with expert_offsets")
+        E, lead = w.shape[0], (w.shape[0],)
+        _sg._need(expert_offsets, torch.int64, (E + 1,), "expert_offsets")
+    N, K = w.shape[-2:]
+    _sg._need(w, torch.bfloat16, (*lead, N, K), "w")
+    return a.shape[0], N, K, E, lead
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _status(status):
+    import torch
+    if status is not None:
+        _sg._need(status, torch.int32, (1,), "status")
+    return status
+
+
+def situ_linear(a, w, expert_offsets=None, bias=None, residual=None, act="none", save_pre=False, out=None,
+                out_dtype=None, status=None, stream=None):
+    """out [R,N] = act(a W_eT + b_e) + residual for the rows of every expert e (rows
+    expert_offsets[e] .. expert_offsets[e+1]-1; rows of no expert are not written), or with one weight
+    for all rows without expert_offsets. a bf16 [R,K]; w bf16 [E,N,K] (or [N,K]); bias fp32 [E,N] (or
+    [N]); residual bf16 [R,N]; act none | relu | silu | gelu; out bf16 (default) or fp32. With
+    ``save_pre`` returns (out, pre): pre bf16 [R,N] is the value before the activation, for
+    situ_linear_bwd. N and K multiples of 8."""
+    import torch
+    R, N, K, E, lead = _linear_shape(a, w, expert_offsets)
+    _sg._need(a, torch.bfloat16, (R, K), "a")
+    if bias is not None:
+        _sg._need(bias, torch.float32, (*lead, N), "bias")
+    if residual is not None:
+        _sg._need(residual, torch.bfloat16, (R, N), "residual")
+    code = _act(act)
+    if out is not None:
+        out_dtype = out.dtype
+    with _launch(stream, a.device) as s:
+        out = _out(out, (R, N), out_dtype or torch.bfloat16, a, "out")
+        pre = torch.empty((R, N), dtype=torch.bfloat16, device=a.device) if save_pre else None
+        _one_device(a, w, expert_offsets, bias, residual, out, _status(status))
+        _sg._check(_sg.load().situ_linear_fwd(a.data_ptr(), w.data_ptr(), _ptr(expert_offsets), E, _ptr(bias),
+                                              _ptr(residual), code, out.data_ptr(), _type(out, "out"), _ptr(pre),
+                                              _ptr(status), R, N, K, s))
+    return (out, pre) if save_pre else out
+
+
+def situ_linear_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, dw_dtype=None, bias=True, need_da=True,
+                    need_dw=True, status=None, stream=None):
+    """(da bf16 [R,K], dw [E,N,K] (or [N,K]) of dw_dtype (default fp32), dbias fp32 [E,N] (or [N])) of
+    situ_linear for dout bf16 [R,N]; the residual's gradient is dout itself. An activation needs ``pre`` of
+    the forward; dz = dout*act'(pre) is then rounded to bf16 before the two products (dbias is the sum
+    of the unrounded dz). What is not asked for (bias, need_da, need_dw) is None. An expert without rows
+    gets zeros in dw and dbias; da of rows of no expert is not written."""
+    import torch
+    R, N, K, E, lead = _linear_shape(dout, w, expert_offsets, "dout")
+    _sg._need(dout, torch.bfloat16, (R, N), "dout")
+    if need_dw:
+        _sg._need(a, torch.bfloat16, (R, K), "a")
+    code = _act(act)
+    if code:
+        if pre is None:
+            raise ValueError(f"act {act!r} needs the saved pre (situ_linear with save_pre=True)")
+        _sg._need(pre, torch.bfloat16, (R, N), "pre")
+    else:
+        pre = None
+    lib = _sg.load()
+    da = dw = dbias = None
+    with _launch(stream, dout.device) as s:
+        _one_device(dout, w, expert_offsets, pre, a if need_dw else None, _status(status))
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dout.device)  # noqa: E731
+        dz, off = dout, _ptr(expert_offsets)
+        if code or bias:
+            if code:
+                dz = new((R, N), torch.bfloat16)
+            nb, ws = 0, None
+            if bias:
+                dbias = new((*lead, N), torch.float32)
+                nb = lib.situ_linear_act_bwd_workspace(R, N, E)
+                ws = _scratch(nb, dout)
+            _sg._check(lib.situ_linear_act_bwd(dout.data_ptr(), _ptr(pre), code, off, E, dz.data_ptr() if code else 0,
+                                               _ptr(dbias), _ptr(ws), nb, R, N, s))
+        if need_da:
+            da = new((R, K), torch.bfloat16)
+            _sg._check(lib.situ_linear_dgrad(dz.data_ptr(), w.data_ptr(), off, E, da.data_ptr(), _ptr(status), R, N, K,
+                                             s))
+        if need_dw:
+            dw = new((*lead, N, K), dw_dtype or torch.float32)
+            nb = lib.situ_linear_wgrad_workspace(R, N, K, E)
+            ws = _scratch(nb, dout)
+            _sg._check(lib.situ_linear_wgrad(dz.data_ptr(), a.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"),
+                                             _ptr(ws), nb, _ptr(status), R, N, K, s))
+    return da, dw, dbias
+
+
+# ---------------------------------------------------------------- autograd operators
+
+_functions = None
+
+
+def _autograd():
+    """The autograd Functions, created on first use (torch is imported lazily by this package)."""
+    global _functions
+    if _functions is not None:
+        return _functions
+    import torch
+
+    class RouteTopk(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, k):
+            p, ids = situ_route_topk(logits, k)
+            ctx.save_for_backward(p, ids)
+            ctx.experts, ctx.dtype = logits.shape[1], logits.dtype
+            ctx.mark_non_differentiable(ids)
+            return p, ids
+
+        @staticmethod
+        def backward(ctx, dp, _):
+            p, ids = ctx.saved_tensors
+            return situ_route_topk_bwd(ids, p, dp.contiguous(), ctx.experts, dtype=ctx.dtype), None
+
+    class Dispatch(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, row_of, expert_offsets):
+            ctx.save_for_backward(row_of)
+            return situ_dispatch(x, row_of, expert_offsets)
+
+        @staticmethod
+        def backward(ctx, dh):
+            (row_of,) = ctx.saved_tensors
+            return situ_combine(dh.contiguous(), row_of), None, None
+
+    class Combine(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, o, weights, residual, row_of, expert_offsets):
+            ctx.save_for_backward(o, weights, row_of, expert_offsets)
+            return situ_combine(o, row_of, weights=weights, residual=residual)
+
+        @staticmethod
+        def backward(ctx, dy):
+            o, weights, row_of, expert_offsets = ctx.saved_tensors
+            do, dw = situ_combine_bwd(dy.contiguous(), o, row_of, weights, expert_offsets)
+            return do, dw, dy if ctx.needs_input_grad[2] else None, None, None
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a, w, bias, residual, expert_offsets, act):
+            keep = act != "none" and any(ctx.needs_input_grad[:3])
+            out = situ_linear(a, w, expert_offsets, bias, residual, act, save_pre=keep)
+            out, pre = out if keep else (out, None)
+            ctx.save_for_backward(a, w, expert_offsets, pre)
+            ctx.act = act
+            return out
+
+        @staticmethod
+        def backward(ctx, dout):
+            a, w, expert_offsets, pre = ctx.saved_tensors
+            need = ctx.needs_input_grad
+            dout = dout.contiguous()
+            da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=torch.bfloat16,
+                                         bias=need[2], need_da=need[0], need_dw=need[1])
+            return da, dw, db, dout if need[3] else None, None, None
+
+    _functions = (RouteTopk, Dispatch, Combine, Linear)
+    return _functions
+
+
+def route_topk(logits, k):
+    """situ_route_topk, differentiable in the scores: (p, ids)."""
+    return _autograd()[0].apply(logits, int(k))
+
+
+def moe_dispatch(x, row_of, expert_offsets):
+    """situ_dispatch, differentiable in x."""
+    return _autograd()[1].apply(x, row_of, expert_offsets)
+
+
+def moe_combine(o, weights, row_of, expert_offsets, residual=None):
+    """situ_combine, differentiable in o, weights and residual."""
+    return _autograd()[2].apply(o, weights, residual, row_of, expert_offsets)
+
+
+def linear(a, w, bias=None, residual=None, expert_offsets=None, act="none"):
+    """situ_linear (bf16 out), differentiable in a, w (gradient in bf16, as PyTorch's autograd wants),
+    bias and residual. Gradients of rows that belong to no expert are undefined."""
+    return _autograd()[3].apply(a, w, bias, residual, expert_offsets, act)
