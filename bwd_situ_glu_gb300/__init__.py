@@ -150,6 +150,7 @@ def load():
     lib.situ_glu_last_cuda_error.restype = cint
     lib.situ_glu_version.argtypes = []
     lib.situ_glu_version.restype = cint
+    from . import moe
     moe.declare(lib)
     _lib = lib
     return lib
@@ -510,9 +511,19 @@ def situ_adam_stream_step(grad, weight, master, m, v, params: AdamParams, stagin
                                             _stream_handle(stream, grad.device)))
 
 
-from . import moe  # noqa: E402  (the operators around the activation; uses the helpers above)
-from .moe import (situ_combine, situ_combine_bwd, situ_dispatch, situ_dispatch_plan, situ_linear,  # noqa: E402
-                  situ_linear_bwd, situ_route_topk, situ_route_topk_bwd)
+_MOE_NAMES = ("situ_route_topk", "situ_route_topk_bwd", "situ_dispatch_plan", "situ_dispatch", "situ_combine",
+              "situ_combine_bwd", "situ_linear", "situ_linear_bwd")
+
+
+def __getattr__(name):
+    """The operators around the activation live in the module ``moe``, which imports torch: on first use."""
+    if name == "moe" or name in _MOE_NAMES:
+        import importlib
+        m = importlib.import_module(__name__ + ".moe")
+        globals().update({n: getattr(m, n) for n in _MOE_NAMES}, moe=m)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 __all__ = [
     "build", "load", "version", "status_string", "SituGluError",
@@ -520,7 +531,6 @@ __all__ = [
     "situ_glu_fwd_save_fp8", "situ_glu_bwd_router_fp8", "FP8_BLOCK", "fp8_scale_blocks",
     "situ_glu_bwd_router_dgrad", "situ_glu_bwd_router_dgrad_wd", "situ_glu_fwd_gateup",
     "situ_and_mul", "selftest_wait_timeout", "AdamParams", "adam_params", "situ_adam_update_host", "situ_adam_stream_step", "adam_staging_bytes",
-    "moe", "situ_route_topk", "situ_route_topk_bwd", "situ_dispatch_plan", "situ_dispatch", "situ_combine",
-    "situ_combine_bwd", "situ_linear", "situ_linear_bwd",
+    "moe", *_MOE_NAMES,
     "LIB_PATH", "INCLUDE",
 ]

@@ -31,12 +31,11 @@ using namespace situ_host;
 using namespace situ_tc;
 using namespace situ_linear;
 
-constexpr int EPW = 2;                       // epilogue warps per 32-lane TMEM quadrant
+constexpr int EPW = 3;                       // epilogue warps per 32-lane TMEM quadrant
 constexpr int CW = 32;                       // accumulator columns per chunk: 64 bytes of bf16
 constexpr int NUM_EPI_THREADS = 4 * EPW * 32;
 constexpr int NUM_THREADS = 64 + NUM_EPI_THREADS;  // warp 0 TMA, warp 1 MMA, then the epilogue
-constexpr int COLS_PER_WARP = BN / EPW;
-constexpr int CPJ = COLS_PER_WARP / CW;      // chunks per job per epilogue warp
+constexpr int NCH = BN / CW;                 // chunks of a job
 constexpr int STAGE_TILE = 32 * CW * 2;      // 32 rows x 64 bytes of output in shared memory
 constexpr int SMEM_BYTES = SMEM_FIXED_BYTES + 1024 + 4 * EPW * STAGE_TILE;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -81,6 +80,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int lrow = quad * 32 + lane;
         const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
         uint8_t* stage = (uint8_t*)(((uintptr_t)sm.extra + 1023) & ~(uintptr_t)1023) + (warp - 2) * STAGE_TILE;
+        const bool bias_vec = ((uintptr_t)bias & 15) == 0;       // NCOL % 8 == 0 keeps every chunk of it aligned
         bool stores_pending = false;             // lane 0 has TMA stores in flight
         int job = 0;
         bool ok = true;
@@ -102,46 +102,65 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             stores_pending = true;
         };
+        // a job's 32-column chunks are dealt out over the EPW warps of a quadrant: slot, slot + EPW, ..
+        // This lane's residual of its next chunk (of this job or the next) is fetched while a chunk is
+        // worked off.
+        Vec<4> res[4];
+        auto fetch_residual = [&](int64_t row0, int64_t row_end, int64_t j0) {
+            if (row0 + lrow < row_end) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (j0 + 8 * q < NCOL)
+                        res[q] = ld_stream<4, true>((const Vec<4>*)(residual + (row0 + lrow) * NCOL + j0 + 8 * q));
+            }
+        };
+        int e = 0;
+        int64_t row0 = 0, row_end = 0;
+        if (sc.t0 < T) {
+            tile_rows(sm.tile_start, offsets, E, R, sc.t0, e, row0, row_end);
+            if (residual) fetch_residual(row0, row_end, (int64_t)sc.n0 * BN + slot * CW);
+        }
         for (int t = sc.t0; t < T; t += sc.tstep) {
-            int e;
-            int64_t row0, row_end;
-            tile_rows(sm.tile_start, offsets, E, R, t, e, row0, row_end);
+            int e_next = e;
+            int64_t row0_next = row0, row_end_next = row_end;
+            if (t + sc.tstep < T) tile_rows(sm.tile_start, offsets, E, R, t + sc.tstep, e_next, row0_next, row_end_next);
             const int64_t row = row0 + lrow;
-            const bool valid = ok && row < row_end;
             const bool full_quad = row0 + quad * 32 + 31 < row_end;
             for (int nt = sc.n0; nt < NT; nt += sc.nstep, ++job) {
                 const int acc = job & 1;
+                const bool last_job = nt + sc.nstep >= NT;            // of this M-tile
                 if (ok && !mbar_wait(&bars->tfull[acc], (uint32_t)((job >> 1) & 1), bars, status)) ok = false;
                 ok = __all_sync(FULL_MASK, ok);      // tcgen05.ld below is warp-collective
+                const bool valid = ok && row < row_end;
                 tc_fence_after();
 #pragma unroll 1
-                for (int k = 0; k < CPJ; ++k) {
-                    const int64_t j0 = (int64_t)nt * BN + slot * COLS_PER_WARP + k * CW;
+                for (int k = slot; k < NCH; k += EPW) {
+                    const int64_t j0 = (int64_t)nt * BN + k * CW;
                     const bool chunk = j0 < NCOL;                 // NCOL % 8 == 0: whole groups of 8
-                    Vec<4> res[4];
-                    if (residual && ok && valid && chunk) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (j0 + 8 * q < NCOL) res[q] = ld_stream<4, true>((const Vec<4>*)(residual + row * NCOL + j0 + 8 * q));
-                    }
+                    const bool last = k + EPW >= NCH;
                     float v[CW];
-                    if (ok) tc_ld<CW>(tmem + t_lane + (uint32_t)(acc * BN + slot * COLS_PER_WARP + k * CW), v);
-                    if (k + 1 == CPJ) {
+                    if (ok) tc_ld<CW>(tmem + t_lane + (uint32_t)(acc * BN + k * CW), v);
+                    if (last) {
                         tc_fence_before();
                         mbar_arrive(&bars->tempty[acc]);          // the accumulator may be overwritten
                     }
-                    if (!ok || !chunk) continue;
-                    if (bias) {
+                    if (bias && chunk) {
+                        // one address for the warp, 16 bytes where the bias allows
                         const float* b = bias + (int64_t)e * NCOL + j0;
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             if (j0 + 4 * q >= NCOL) continue;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[4 * q + i] += __ldg(b + 4 * q + i);
+                            float4 f;
+                            if (bias_vec) f = __ldg((const float4*)(b + 4 * q));
+                            else f = make_float4(__ldg(b + 4 * q), __ldg(b + 4 * q + 1), __ldg(b + 4 * q + 2), __ldg(b + 4 * q + 3));
+                            v[4 * q] += f.x;
+                            v[4 * q + 1] += f.y;
+                            v[4 * q + 2] += f.z;
+                            v[4 * q + 3] += f.w;
                         }
                     }
                     uint32_t w[CW / 2];
-                    if (pre) {
+                    if (pre && ok && chunk) {
 #pragma unroll
                         for (int i = 0; i < CW / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
                         if (full_quad) {
@@ -158,17 +177,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < CW; ++i) v[i] = act_value<ACT>(v[i]);
                     }
-                    if (residual && valid) {
+                    if (residual) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            if (j0 + 8 * q >= NCOL) continue;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                v[8 * q + 2 * i] += bf16_lo(res[q].w[i]);
-                                v[8 * q + 2 * i + 1] += bf16_hi(res[q].w[i]);
+                                v[8 * q + 2 * i] += bf16_lo(res[q].w[i]);      // columns past NCOL and rows past
+                                v[8 * q + 2 * i + 1] += bf16_hi(res[q].w[i]);  // the expert are not stored
                             }
                         }
+                        if (!last) fetch_residual(row0, row_end, j0 + EPW * CW);
+                        else if (!last_job) fetch_residual(row0, row_end, (int64_t)(nt + sc.nstep) * BN + slot * CW);
+                        else if (t + sc.tstep < T) fetch_residual(row0_next, row_end_next, (int64_t)sc.n0 * BN + slot * CW);
                     }
+                    if (!ok || !chunk) continue;
                     if (out_fp32) {
                         if (valid) {
 #pragma unroll
@@ -193,6 +215,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                 }
             }
+            e = e_next;
+            row0 = row0_next;
+            row_end = row_end_next;
         }
         if (lane == 0 && stores_pending) bulk_wait_all();   // every staged tile written
     }

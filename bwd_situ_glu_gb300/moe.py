@@ -15,9 +15,11 @@ workspaces are allocated on that stream.
 from __future__ import annotations
 
 import ctypes
-from contextlib import contextmanager
+
+import torch
 
 import bwd_situ_glu_gb300 as _sg
+from bwd_situ_glu_gb300 import _check, load as _lib
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 MAX_EXPERTS, MAX_TOPK = 1024, 32  # SITU_MAX_EXPERTS, SITU_MAX_TOPK
@@ -45,7 +47,6 @@ def declare(lib):
 
 
 def _type(t, name):
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype == torch.bfloat16:
@@ -55,65 +56,54 @@ def _type(t, name):
     raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
+def _two(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional, got {tuple(t.shape)}")
+    return t.shape
+
+
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _one_device(*tensors):
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
+def _moved(stream, t):
+    """Whether the work runs elsewhere than on the current stream of the current device (see _elsewhere)."""
+    return stream is not None or t.device.index != torch._C._cuda_getDevice()
+
+
+def _elsewhere(stream, t, call):
+    """call() with t's device and ``stream`` current, so that what it allocates belongs to that stream."""
+    with torch.cuda.device(t.device):
+        if stream is None:
+            return call()
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        with torch.cuda.stream(stream):
+            return call()
+
+
+def _current(t):
+    """Handle of the current stream of t's device. (The Stream object of torch.cuda.current_stream costs as
+    much as a decoding step's kernel: 5 us on the host.)"""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _need(t, dtype, shape, like, name):
+    """A contiguous tensor of this type and shape on the device of ``like``."""
+    if t.__class__ is not like.__class__ or t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        _sg._need(t, dtype, shape, name)   # says what is wrong (a subclass of Tensor is fine)
+    if t.device != like.device:
         raise ValueError("all tensors must be on the same device")
 
 
-@contextmanager
-def _other_stream(stream, device):
-    import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield int(stream.cuda_stream)
-
-
-@contextmanager
-def _other_device(device):
-    import torch
-    with torch.cuda.device(device):
-        yield int(torch.cuda.current_stream(device).cuda_stream)
-
-
-class _Here:
-    """The current stream of the current device: nothing to switch."""
-
-    def __init__(self, handle):
-        self.handle = handle
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        return False
-
-
-def _launch(stream, device):
-    """Context in which allocations belong to the launch stream; gives its handle."""
-    import torch
-    if stream is not None:
-        return _other_stream(stream, device)
-    if device.index == torch.cuda.current_device():
-        return _Here(torch.cuda.current_stream(device).cuda_stream)
-    return _other_device(device)
-
-
 def _out(t, shape, dtype, like, name):
-    import torch
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    _sg._need(t, dtype, shape, name)
+    _need(t, dtype, shape, like, name)
     return t
 
 
 def _scratch(nbytes, like):
-    import torch
     return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
 
 
@@ -123,43 +113,39 @@ def situ_route_topk(logits, k, p=None, ids=None, stream=None):
     """(p fp32 [T,k], ids int32 [T,k]): softmax over the k largest scores of each token, in descending
     order, ties to the lower index. A score of -inf is never chosen (id -1, p 0). logits [T,E] bf16 or
     fp32, E <= 1024, k <= min(E, 32)."""
-    import torch
     ty = _type(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
-    _sg._need(logits, logits.dtype, (T, E), "logits")
-    with _launch(stream, logits.device) as s:
-        p = _out(p, (T, k), torch.float32, logits, "p")
-        ids = _out(ids, (T, k), torch.int32, logits, "ids")
-        _one_device(logits, p, ids)
-        _sg._check(_sg.load().situ_route_topk(logits.data_ptr(), ty, p.data_ptr(), ids.data_ptr(), T, E, k, s))
+    _need(logits, logits.dtype, (T, E), logits, "logits")
+    if _moved(stream, logits):
+        return _elsewhere(stream, logits, lambda: situ_route_topk(logits, k, p, ids))
+    p = _out(p, (T, k), torch.float32, logits, "p")
+    ids = _out(ids, (T, k), torch.int32, logits, "ids")
+    _check(_lib().situ_route_topk(logits.data_ptr(), ty, p.data_ptr(), ids.data_ptr(), T, E, k, _current(logits)))
     return p, ids
 
 
 def situ_route_topk_bwd(ids, p, dp, num_experts, dtype=None, row_of=None, dlogits=None, stream=None):
     """dlogits [T,num_experts] of ``dtype`` (default fp32): p_k(dp_k - sum_j p_j dp_j) at ids, 0 elsewhere.
     dp fp32 [T,k], or with ``row_of`` (int32 [T,k]) fp32 [R] in row order."""
-    import torch
-    if ids.dim() != 2:
-        raise ValueError("ids must be [T, k]")
-    T, k = ids.shape
-    _sg._need(ids, torch.int32, (T, k), "ids")
-    _sg._need(p, torch.float32, (T, k), "p")
+    T, k = _two(ids, "ids")
+    _need(ids, torch.int32, (T, k), ids, "ids")
+    _need(p, torch.float32, (T, k), ids, "p")
     R = 0
     if row_of is None:
-        _sg._need(dp, torch.float32, (T, k), "dp")
+        _need(dp, torch.float32, (T, k), ids, "dp")
     else:
-        _sg._need(row_of, torch.int32, (T, k), "row_of")
+        _need(row_of, torch.int32, (T, k), ids, "row_of")
         R = dp.numel()
-        _sg._need(dp, torch.float32, (R,), "dp")
+        _need(dp, torch.float32, (R,), ids, "dp")
+    if _moved(stream, ids):
+        return _elsewhere(stream, ids, lambda: situ_route_topk_bwd(ids, p, dp, num_experts, dtype, row_of, dlogits))
     if dlogits is not None:
         dtype = dlogits.dtype
-    with _launch(stream, ids.device) as s:
-        dlogits = _out(dlogits, (T, num_experts), dtype or torch.float32, ids, "dlogits")
-        _one_device(ids, p, dp, row_of, dlogits)
-        _sg._check(_sg.load().situ_route_topk_bwd(ids.data_ptr(), p.data_ptr(), dp.data_ptr(), _ptr(row_of), R,
-                                                  dlogits.data_ptr(), _type(dlogits, "dlogits"), T, num_experts, k, s))
+    dlogits = _out(dlogits, (T, num_experts), dtype or torch.float32, ids, "dlogits")
+    _check(_lib().situ_route_topk_bwd(ids.data_ptr(), p.data_ptr(), dp.data_ptr(), _ptr(row_of), R, dlogits.data_ptr(),
+                                      _type(dlogits, "dlogits"), T, num_experts, k, _current(ids)))
     return dlogits
 
 
@@ -169,93 +155,81 @@ def situ_dispatch_plan(ids, num_experts, p=None, stream=None):
     """(expert_offsets int64 [E+1], row_of int32 [T,k], src int32 [T*k], p_rows fp32 [T*k] or None): the rows
     of the token-expert pairs, sorted by expert and, within one, by token and choice. An id outside
     [0, num_experts) has no row (row_of -1); src past the last row is -1, p_rows 0."""
-    import torch
-    if ids.dim() != 2:
-        raise ValueError("ids must be [T, k]")
-    T, k = ids.shape
-    _sg._need(ids, torch.int32, (T, k), "ids")
+    T, k = _two(ids, "ids")
+    _need(ids, torch.int32, (T, k), ids, "ids")
     if p is not None:
-        _sg._need(p, torch.float32, (T, k), "p")
-        _one_device(ids, p)
-    lib = _sg.load()
-    with _launch(stream, ids.device) as s:
-        new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=ids.device)  # noqa: E731
-        offsets = new(num_experts + 1 if num_experts > 0 else 0, dtype=torch.int64)
-        row_of, src = new(T, k), new(T * k)
-        p_rows = None if p is None else new(T * k, dtype=torch.float32)
-        nb = lib.situ_dispatch_plan_workspace(T, k, num_experts)
-        ws = _scratch(nb, ids)
-        # without tokens there is nothing to weigh: the pointers of empty tensors are null
-        _sg._check(lib.situ_dispatch_plan(ids.data_ptr(), _ptr(p), offsets.data_ptr(), row_of.data_ptr(),
-                                          src.data_ptr(), _ptr(p_rows), _ptr(ws), nb, T, k, num_experts, s))
+        _need(p, torch.float32, (T, k), ids, "p")
+    if _moved(stream, ids):
+        return _elsewhere(stream, ids, lambda: situ_dispatch_plan(ids, num_experts, p))
+    lib, dev, n = _lib(), ids.device, T * k
+    offsets = torch.empty(max(0, num_experts + 1), dtype=torch.int64, device=dev)
+    row_of = torch.empty((T, k), dtype=torch.int32, device=dev)
+    src = torch.empty(n, dtype=torch.int32, device=dev)
+    p_rows = None if p is None else torch.empty(n, dtype=torch.float32, device=dev)
+    nb = lib.situ_dispatch_plan_workspace(T, k, num_experts)
+    ws = _scratch(nb, ids)
+    # without tokens there is nothing to weigh: the pointers of empty tensors are null
+    _check(lib.situ_dispatch_plan(ids.data_ptr(), _ptr(p), offsets.data_ptr(), row_of.data_ptr(), src.data_ptr(),
+                                  _ptr(p_rows), _ptr(ws), nb, T, k, num_experts, _current(ids)))
     return offsets, row_of, src, p_rows
 
 
 def situ_dispatch(x, row_of, expert_offsets, weights=None, h=None, stream=None):
     """h [T*k, D]: h[row_of[t,j]] = x[t], or weights[t,j]*x[t] with weights fp32 [T,k]; rows that belong to no
     token are zero. x [T,D] bf16 or fp32."""
-    import torch
     ty = _type(x, "x")
-    if x.dim() != 2 or row_of.dim() != 2:
-        raise ValueError("x must be [T, D] and row_of [T, k]")
-    (T, D), k = x.shape, row_of.shape[1]
-    _sg._need(x, x.dtype, (T, D), "x")
-    _sg._need(row_of, torch.int32, (T, k), "row_of")
+    (T, D), k = _two(x, "x"), _two(row_of, "row_of")[1]
+    _need(x, x.dtype, (T, D), x, "x")
+    _need(row_of, torch.int32, (T, k), x, "row_of")
     E = expert_offsets.numel() - 1
-    _sg._need(expert_offsets, torch.int64, (E + 1,), "expert_offsets")
+    _need(expert_offsets, torch.int64, (E + 1,), x, "expert_offsets")
     if weights is not None:
-        _sg._need(weights, torch.float32, (T, k), "weights")
-    with _launch(stream, x.device) as s:
-        h = _out(h, (T * k, D), x.dtype, x, "h")
-        _one_device(x, row_of, expert_offsets, weights, h)
-        _sg._check(_sg.load().situ_dispatch(x.data_ptr(), ty, row_of.data_ptr(), expert_offsets.data_ptr(), E,
-                                            _ptr(weights), h.data_ptr(), T, k, T * k, D, s))
+        _need(weights, torch.float32, (T, k), x, "weights")
+    if _moved(stream, x):
+        return _elsewhere(stream, x, lambda: situ_dispatch(x, row_of, expert_offsets, weights, h))
+    h = _out(h, (T * k, D), x.dtype, x, "h")
+    _check(_lib().situ_dispatch(x.data_ptr(), ty, row_of.data_ptr(), expert_offsets.data_ptr(), E, _ptr(weights),
+                                h.data_ptr(), T, k, T * k, D, _current(x)))
     return h
 
 
 def situ_combine(o, row_of, weights=None, residual=None, y=None, stream=None):
     """y [T,D] = residual + sum_j weights[t,j]*o[row_of[t,j]] (weights default to 1, residual to 0; fp32,
     rounded once). o [R,D] bf16 or fp32; ``y`` may be ``residual`` itself."""
-    import torch
     ty = _type(o, "o")
-    if o.dim() != 2 or row_of.dim() != 2:
-        raise ValueError("o must be [R, D] and row_of [T, k]")
-    (R, D), (T, k) = o.shape, row_of.shape
-    _sg._need(o, o.dtype, (R, D), "o")
-    _sg._need(row_of, torch.int32, (T, k), "row_of")
+    (R, D), (T, k) = _two(o, "o"), _two(row_of, "row_of")
+    _need(o, o.dtype, (R, D), o, "o")
+    _need(row_of, torch.int32, (T, k), o, "row_of")
     if weights is not None:
-        _sg._need(weights, torch.float32, (T, k), "weights")
+        _need(weights, torch.float32, (T, k), o, "weights")
     if residual is not None:
-        _sg._need(residual, o.dtype, (T, D), "residual")
-    with _launch(stream, o.device) as s:
-        y = _out(y, (T, D), o.dtype, o, "y")
-        _one_device(o, row_of, weights, residual, y)
-        _sg._check(_sg.load().situ_combine(o.data_ptr(), ty, row_of.data_ptr(), _ptr(weights), _ptr(residual),
-                                           y.data_ptr(), T, k, R, D, s))
+        _need(residual, o.dtype, (T, D), o, "residual")
+    if _moved(stream, o):
+        return _elsewhere(stream, o, lambda: situ_combine(o, row_of, weights, residual, y))
+    y = _out(y, (T, D), o.dtype, o, "y")
+    _check(_lib().situ_combine(o.data_ptr(), ty, row_of.data_ptr(), _ptr(weights), _ptr(residual), y.data_ptr(), T, k,
+                               R, D, _current(o)))
     return y
 
 
 def situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do=None, dweights=None, stream=None):
     """(do [R,D] of o's type, dweights fp32 [T,k]): do[row_of[t,j]] = weights[t,j]*dy[t] (rows of no token are
     zero), dweights[t,j] = <dy[t], o[row_of[t,j]]> (0 without a row)."""
-    import torch
     ty = _type(o, "o")
-    if o.dim() != 2 or row_of.dim() != 2:
-        raise ValueError("o must be [R, D] and row_of [T, k]")
-    (R, D), (T, k) = o.shape, row_of.shape
-    _sg._need(o, o.dtype, (R, D), "o")
-    _sg._need(dy, o.dtype, (T, D), "dy")
-    _sg._need(row_of, torch.int32, (T, k), "row_of")
-    _sg._need(weights, torch.float32, (T, k), "weights")
+    (R, D), (T, k) = _two(o, "o"), _two(row_of, "row_of")
+    _need(o, o.dtype, (R, D), o, "o")
+    _need(dy, o.dtype, (T, D), o, "dy")
+    _need(row_of, torch.int32, (T, k), o, "row_of")
+    _need(weights, torch.float32, (T, k), o, "weights")
     E = expert_offsets.numel() - 1
-    _sg._need(expert_offsets, torch.int64, (E + 1,), "expert_offsets")
-    with _launch(stream, o.device) as s:
-        do = _out(do, (R, D), o.dtype, o, "do")
-        dweights = _out(dweights, (T, k), torch.float32, o, "dweights")
-        _one_device(dy, o, row_of, weights, expert_offsets, do, dweights)
-        _sg._check(_sg.load().situ_combine_bwd(dy.data_ptr(), o.data_ptr(), ty, row_of.data_ptr(), weights.data_ptr(),
-                                               expert_offsets.data_ptr(), E, do.data_ptr(), dweights.data_ptr(), T, k,
-                                               R, D, s))
+    _need(expert_offsets, torch.int64, (E + 1,), o, "expert_offsets")
+    if _moved(stream, o):
+        return _elsewhere(stream, o, lambda: situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do, dweights))
+    do = _out(do, (R, D), o.dtype, o, "do")
+    dweights = _out(dweights, (T, k), torch.float32, o, "dweights")
+    _check(_lib().situ_combine_bwd(dy.data_ptr(), o.data_ptr(), ty, row_of.data_ptr(), weights.data_ptr(),
+                                   expert_offsets.data_ptr(), E, do.data_ptr(), dweights.data_ptr(), T, k, R, D,
+                                   _current(o)))
     return do, dweights
 
 
@@ -263,34 +237,27 @@ def situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do=None, dweights=N
 
 def _linear_shape(a, w, expert_offsets, a_name="a"):
     """(R, N, K, E, lead): w is [N,K] without expert_offsets, [E,N,K] with them; lead is () or (E,)."""
-    import torch
-    if a.dim() != 2:
-        raise ValueError(f"{a_name} must be two-dimensional")
+    _type(a, a_name)
+    R = _two(a, a_name)[0]
     if expert_offsets is None:
         if w.dim() != 2:
             raise ValueError("w must be [N, K] without expert_offsets")
         E, lead = 1, ()
+        N, K = w.shape
     else:
         if w.dim() != 3:
             raise ValueError("w must be [E, N, K] with expert_offsets")
-        E, lead = w.shape[0], (w.shape[0],)
-        _sg._need(expert_offsets, torch.int64, (E + 1,), "expert_offsets")
-    N, K = w.shape[-2:]
-    _sg._need(w, torch.bfloat16, (*lead, N, K), "w")
-    return a.shape[0], N, K, E, lead
+        E, N, K = w.shape
+        lead = (E,)
+        _need(expert_offsets, torch.int64, (E + 1,), a, "expert_offsets")
+    _need(w, torch.bfloat16, (*lead, N, K), a, "w")
+    return R, N, K, E, lead
 
 
 def _act(act):
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
     return ACTIVATIONS[act]
-
-
-def _status(status):
-    import torch
-    if status is not None:
-        _sg._need(status, torch.int32, (1,), "status")
-    return status
 
 
 def situ_linear(a, w, expert_offsets=None, bias=None, residual=None, act="none", save_pre=False, out=None,
@@ -300,24 +267,26 @@ def situ_linear(a, w, expert_offsets=None, bias=None, residual=None, act="none",
     for all rows without expert_offsets. a bf16 [R,K]; w bf16 [E,N,K] (or [N,K]); bias fp32 [E,N] (or
     [N]); residual bf16 [R,N]; act none | relu | silu | gelu; out bf16 (default) or fp32. With
     ``save_pre`` returns (out, pre): pre bf16 [R,N] is the value before the activation, for
-    situ_linear_bwd. N and K multiples of 8."""
-    import torch
+    situ_linear_bwd. N and K multiples of 8. ``status`` (int32 [1] on the device, zeroed by the caller)
+    turns 1 if a pipeline wait timed out."""
     R, N, K, E, lead = _linear_shape(a, w, expert_offsets)
-    _sg._need(a, torch.bfloat16, (R, K), "a")
+    _need(a, torch.bfloat16, (R, K), a, "a")
     if bias is not None:
-        _sg._need(bias, torch.float32, (*lead, N), "bias")
+        _need(bias, torch.float32, (*lead, N), a, "bias")
     if residual is not None:
-        _sg._need(residual, torch.bfloat16, (R, N), "residual")
+        _need(residual, torch.bfloat16, (R, N), a, "residual")
+    if status is not None:
+        _need(status, torch.int32, (1,), a, "status")
     code = _act(act)
+    if _moved(stream, a):
+        return _elsewhere(stream, a, lambda: situ_linear(a, w, expert_offsets, bias, residual, act, save_pre, out,
+                                                         out_dtype, status))
     if out is not None:
         out_dtype = out.dtype
-    with _launch(stream, a.device) as s:
-        out = _out(out, (R, N), out_dtype or torch.bfloat16, a, "out")
-        pre = torch.empty((R, N), dtype=torch.bfloat16, device=a.device) if save_pre else None
-        _one_device(a, w, expert_offsets, bias, residual, out, _status(status))
-        _sg._check(_sg.load().situ_linear_fwd(a.data_ptr(), w.data_ptr(), _ptr(expert_offsets), E, _ptr(bias),
-                                              _ptr(residual), code, out.data_ptr(), _type(out, "out"), _ptr(pre),
-                                              _ptr(status), R, N, K, s))
+    out = _out(out, (R, N), out_dtype or torch.bfloat16, a, "out")
+    pre = torch.empty((R, N), dtype=torch.bfloat16, device=a.device) if save_pre else None
+    _check(_lib().situ_linear_fwd(a.data_ptr(), w.data_ptr(), _ptr(expert_offsets), E, _ptr(bias), _ptr(residual), code,
+                                  out.data_ptr(), _type(out, "out"), _ptr(pre), _ptr(status), R, N, K, _current(a)))
     return (out, pre) if save_pre else out
 
 
@@ -328,44 +297,44 @@ def situ_linear_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, dw_dt
     the forward; dz = dout*act'(pre) is then rounded to bf16 before the two products (dbias is the sum
     of the unrounded dz). What is not asked for (bias, need_da, need_dw) is None. An expert without rows
     gets zeros in dw and dbias; da of rows of no expert is not written."""
-    import torch
     R, N, K, E, lead = _linear_shape(dout, w, expert_offsets, "dout")
-    _sg._need(dout, torch.bfloat16, (R, N), "dout")
+    _need(dout, torch.bfloat16, (R, N), dout, "dout")
     if need_dw:
-        _sg._need(a, torch.bfloat16, (R, K), "a")
+        _need(a, torch.bfloat16, (R, K), dout, "a")
     code = _act(act)
     if code:
         if pre is None:
             raise ValueError(f"act {act!r} needs the saved pre (situ_linear with save_pre=True)")
-        _sg._need(pre, torch.bfloat16, (R, N), "pre")
+        _need(pre, torch.bfloat16, (R, N), dout, "pre")
     else:
         pre = None
-    lib = _sg.load()
+    if status is not None:
+        _need(status, torch.int32, (1,), dout, "status")
+    if _moved(stream, dout):
+        return _elsewhere(stream, dout, lambda: situ_linear_bwd(dout, a, w, expert_offsets, act, pre, dw_dtype, bias,
+                                                                need_da, need_dw, status))
+    lib, dev, s = _lib(), dout.device, _current(dout)
     da = dw = dbias = None
-    with _launch(stream, dout.device) as s:
-        _one_device(dout, w, expert_offsets, pre, a if need_dw else None, _status(status))
-        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dout.device)  # noqa: E731
-        dz, off = dout, _ptr(expert_offsets)
-        if code or bias:
-            if code:
-                dz = new((R, N), torch.bfloat16)
-            nb, ws = 0, None
-            if bias:
-                dbias = new((*lead, N), torch.float32)
-                nb = lib.situ_linear_act_bwd_workspace(R, N, E)
-                ws = _scratch(nb, dout)
-            _sg._check(lib.situ_linear_act_bwd(dout.data_ptr(), _ptr(pre), code, off, E, dz.data_ptr() if code else 0,
-                                               _ptr(dbias), _ptr(ws), nb, R, N, s))
-        if need_da:
-            da = new((R, K), torch.bfloat16)
-            _sg._check(lib.situ_linear_dgrad(dz.data_ptr(), w.data_ptr(), off, E, da.data_ptr(), _ptr(status), R, N, K,
-                                             s))
-        if need_dw:
-            dw = new((*lead, N, K), dw_dtype or torch.float32)
-            nb = lib.situ_linear_wgrad_workspace(R, N, K, E)
+    dz, off = dout, _ptr(expert_offsets)
+    if code or bias:
+        if code:
+            dz = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+        nb, ws = 0, None
+        if bias:
+            dbias = torch.empty((*lead, N), dtype=torch.float32, device=dev)
+            nb = lib.situ_linear_act_bwd_workspace(R, N, E)
             ws = _scratch(nb, dout)
-            _sg._check(lib.situ_linear_wgrad(dz.data_ptr(), a.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"),
-                                             _ptr(ws), nb, _ptr(status), R, N, K, s))
+        _check(lib.situ_linear_act_bwd(dout.data_ptr(), _ptr(pre), code, off, E, dz.data_ptr() if code else 0,
+                                       _ptr(dbias), _ptr(ws), nb, R, N, s))
+    if need_da:
+        da = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
+        _check(lib.situ_linear_dgrad(dz.data_ptr(), w.data_ptr(), off, E, da.data_ptr(), _ptr(status), R, N, K, s))
+    if need_dw:
+        dw = torch.empty((*lead, N, K), dtype=dw_dtype or torch.float32, device=dev)
+        nb = lib.situ_linear_wgrad_workspace(R, N, K, E)
+        ws = _scratch(nb, dout)
+        _check(lib.situ_linear_wgrad(dz.data_ptr(), a.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"), _ptr(ws), nb,
+                                     _ptr(status), R, N, K, s))
     return da, dw, dbias
 
 
@@ -375,11 +344,10 @@ _functions = None
 
 
 def _autograd():
-    """The autograd Functions, created on first use (torch is imported lazily by this package)."""
+    """The autograd Functions, created on first use."""
     global _functions
     if _functions is not None:
         return _functions
-    import torch
 
     class RouteTopk(torch.autograd.Function):
         @staticmethod
