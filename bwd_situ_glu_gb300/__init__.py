@@ -46,7 +46,7 @@ SOURCES = [os.path.join(CSRC, n) for n in ("situ_glu.cu", "situ_glu_fp8.cu", "si
 # per-source extra flags: the host Adam update is a fixed sequence of IEEE fp32 operations
 SOURCE_FLAGS = {"situ_adam.cu": ["-Xcompiler", "-ffp-contract=off,-fno-fast-math,-fno-math-errno"]}
 DEPENDS = SOURCES + [os.path.join(CSRC, n) for n in ("situ_math.cuh", "situ_device.cuh", "situ_host.h",
-                                                     "situ_tc.cuh", "situ_linear.cuh")] + [
+                                                     "situ_tc.cuh", "situ_pair.cuh", "situ_linear.cuh")] + [
     os.path.join(INCLUDE, n) for n in ("situ_glu.h", "situ_moe.h")]
 
 NVCC_FLAGS = [

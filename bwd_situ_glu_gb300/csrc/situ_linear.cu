@@ -1,18 +1,19 @@
 // situ_linear.cu — matrix product of every row with its expert's (or the one dense) weight, with
 // bias, activation and residual in the epilogue, and the input gradient (include/situ_moe.h).
 //
-//   forward   out[r] = act(a[r]·W_eᵀ + b_e) + residual[r]       A = a,  B = W_e  (K-major)
-//   dgrad     da[r]  = dz[r]·W_e                                 A = dz, B = W_eᵀ (W_e as stored is N-major)
+//   forward   out[r] = act(a[r]·W_eᵀ + b_e) + residual[r]
+//   dgrad     da[r]  = dz[r]·W_e
 //
 // Two kernels:
-//   * linear_tc_kernel: the expert-grouped pipeline of situ_tc.cuh (TMA ring, tcgen05.mma, two TMEM
-//     accumulators, bounded waits), whose epilogue adds the bias, applies the activation, adds the
-//     residual in fp32 and rounds once. bf16 tiles leave through shared memory as TMA stores (64-byte
-//     rows, 64-byte swizzle, so neither the staging writes nor the TMA reads conflict); a quadrant of
-//     rows that crosses its expert's end stores from registers. Weights are a 3-D tensor [E, N, K], so
-//     the boxes of a ragged edge read zeros, never the next expert.
+//   * linear_tc_kernel: tcgen05 on pairs of SMs (situ_pair.cuh). The WEIGHTS are the MMA's 256-row operand and
+//     the rows its N operand: an accumulator is (256 output columns) x (up to 256 rows of one expert), and as
+//     N may be any multiple of 32, an expert's ragged rows cost what they are, not a multiple of 128. The
+//     transposed accumulator suits the epilogue too: a lane holds one output column, so the bias is one
+//     value and a warp's stores (and residual loads) of a row are 64 consecutive bytes, whatever the
+//     number of rows. Weights are a 3-D tensor [E, N, K], so the boxes of a ragged edge read zeros, never
+//     the next expert; rows past a chunk's end are computed and not stored.
 //   * linear_few_kernel: for few rows per expert (a decoding step), where the weights' one trip from
-//     HBM is the whole cost and a 128-row tile would be almost empty: see there.
+//     HBM is the whole cost: see there.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -22,206 +23,346 @@
 #include "situ_device.cuh"
 #include "situ_host.h"
 #include "situ_linear.cuh"
-#include "situ_tc.cuh"
+#include "situ_pair.cuh"
 
 namespace {
 
 using namespace situ;
 using namespace situ_host;
-using namespace situ_tc;
+using namespace situ_pair;
 using namespace situ_linear;
 
-constexpr int EPW = 3;                       // epilogue warps per 32-lane TMEM quadrant
-constexpr int CW = 32;                       // accumulator columns per chunk: 64 bytes of bf16
-constexpr int NUM_EPI_THREADS = 4 * EPW * 32;
-constexpr int NUM_THREADS = 64 + NUM_EPI_THREADS;  // warp 0 TMA, warp 1 MMA, then the epilogue
-constexpr int NCH = BN / CW;                 // chunks of a job
-constexpr int STAGE_TILE = 32 * CW * 2;      // 32 rows x 64 bytes of output in shared memory
-constexpr int SMEM_BYTES = SMEM_FIXED_BYTES + 1024 + 4 * EPW * STAGE_TILE;
+constexpr int EPW = 2;                       // epilogue warps per 32-lane TMEM quadrant
+constexpr int CW = 32;                       // rows (accumulator columns) per epilogue step
+constexpr int PATCH = CW * 64;               // 32 rows x 32 output columns of bf16 in shared memory, per warp
+constexpr int NUM_EPI_WARPS = 4 * EPW;
+constexpr int NUM_THREADS = 64 + NUM_EPI_WARPS * 32;  // warp 0 TMA, warp 1 MMA, then the epilogue
+constexpr int TILE = 256;                    // output columns per job: 128 per CTA of the pair
+constexpr int MAX_CHUNK = 256;               // rows per job: the MMA's largest N
+constexpr int GROUP = 8;                     // chunks of an expert worked on at a time
+
+// A ring stage: 128 weight rows and half of the chunk's rows, 128 bytes each.
+__host__ __device__ constexpr int stage_bytes(int most) { return PA_BYTES + most / 2 * 128; }
+__host__ __device__ constexpr int ring_stages(int most) {
+    const int s = PRING_BYTES / stage_bytes(most);
+    return s < PSTAGES ? s : PSTAGES;
+}
+static_assert(ring_stages(MAX_CHUNK) == 6, "ring");
+
+struct Job {
+    int e, nt;
+    int row0;                                // first row of the chunk
+    int rows;                                // rows of the chunk
+    int n;                                   // rows rounded up to the MMA's multiple of 32
+};
+
+// The work list, in shared memory: an expert's rows are cut into chunks of at most `most` rows (a multiple of
+// 32), as even as multiples of 32 allow; a job is one chunk times one tile of output columns.
+struct Plan {
+    int start[MAX_EXPERTS + 1];              // chunks of the experts before e
+    int begin[MAX_EXPERTS];                  // first row of e
+    int rows[MAX_EXPERTS];
+};
+
+// Job j: the experts in order; within one, GROUP chunks at a time, and within those the output tiles in
+// order, so that the pairs at work at one time share a few weight tiles and a few chunks. 32-bit throughout
+// (the host bounds the number of jobs): with 64-bit divisions and offsets from global memory, finding the next
+// job took longer than the ring holds work, 0.8 us of every job.
+__device__ __forceinline__ Job job_at(int j, const Plan& plan, int E, int NT) {
+    int lo = 0, hi = E - 1;                  // last e whose first job is <= j
+    const int ch = j / NT;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (plan.start[mid] <= ch) lo = mid; else hi = mid - 1;
+    }
+    Job q;
+    q.e = lo;
+    const int first = plan.start[lo], nch = plan.start[lo + 1] - first;
+    const int local = j - first * NT;
+    const int g = local / (GROUP * NT), rem = local - g * (GROUP * NT);
+    const int width = min(GROUP, nch - g * GROUP);
+    q.nt = rem / width;
+    const int c = g * GROUP + rem - q.nt * width;
+    const int size = ((plan.rows[lo] + nch - 1) / nch + 31) & ~31;
+    q.row0 = plan.begin[lo] + c * size;
+    q.rows = min(size, plan.rows[lo] - c * size);
+    q.n = (q.rows + 31) & ~31;
+    return q;
+}
+
+constexpr int SMEM_BYTES = 1024 + PRING_BYTES + NUM_EPI_WARPS * PATCH + (int)sizeof(PairBars) + (int)sizeof(Plan);
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
-// W_MN: B is W_eᵀ (dgrad; four 64-column boxes per stage). ACT: the activation. NCOL output columns
-// (N forward, K dgrad), KB 64-wide blocks of the contraction.
+// ---- the epilogue's layouts. The accumulator is (output columns) x (rows), memory is rows x columns. tcgen05.ld
+// 16x256b gives a lane two rows of one output column, the fragment of 8 x 8 matrices that stmatrix transposes on
+// its way to shared memory: a warp's patch of 32 rows x 32 columns (64 bytes a row) takes 4 stmatrix and
+// leaves in 4 coalesced 16-byte stores a lane. (2-byte stores straight from a column's lane, 64 bytes a
+// store, cost 6 cycles each: 6000 cycles for a 256-row accumulator, more than its products at K = 768.)
+// The residual comes the same way back, through ldmatrix.
+__device__ __forceinline__ void tc_ld_16x256(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Byte of the 16-byte piece g (of 4) of row i in a patch: swizzled so that neither eight consecutive rows' pieces
+// (stmatrix, ldmatrix) nor eight lanes' 16-byte accesses share banks.
+__device__ __forceinline__ uint32_t patch_at(int i, int g) { return (uint32_t)(i * 64 + ((g ^ ((i >> 1) & 3)) << 4)); }
+
+__device__ __forceinline__ void st_matrix_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ld_matrix_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// A patch between shared memory and rows of NCOL elements in global memory: lane l moves the piece l % 4 of rows
+// l / 4, l / 4 + 8, .. `at`: the element of the patch's row 0, column 0; ncols: columns inside the matrix
+// (a multiple of 8).
+__device__ __forceinline__ void patch_out(const uint8_t* patch, uint16_t* out, int64_t at, int64_t NCOL, int left, int ncols,
+                                          int lane) {
+#pragma unroll
+    for (int i = lane >> 2; i < CW; i += 8) {
+        const uint4 v = *(const uint4*)(patch + patch_at(i, lane & 3));
+        if (i < left && (lane & 3) * 8 < ncols)
+            st_stream<4>((Vec<4>*)(out + at + (int64_t)i * NCOL + (lane & 3) * 8), Vec<4>{{v.x, v.y, v.z, v.w}});
+    }
+}
+
+// W_MN: A is W_eᵀ (dgrad), read MN-major from W_e as stored. ACT: the activation. NCOL output columns
+// (N forward, K dgrad), KB 64-deep blocks of the contraction. map_r[i]: the rows' tensor with boxes of
+// 128 >> i rows.
+struct RowMaps {
+    CUtensorMap m[4];
+};
+
 template <bool W_MN, int ACT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    linear_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                     const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
+    linear_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_r,
                      const int64_t* __restrict__ offsets, const float* __restrict__ bias,
                      const uint16_t* __restrict__ residual, void* __restrict__ out, int out_fp32,
                      uint16_t* __restrict__ pre, int* __restrict__ status, int E, int64_t R, int64_t NCOL, int KB,
-                     int csplit) {
+                     int most) {
     extern __shared__ uint8_t smem_raw[];
-    const Smem sm = carve_smem(smem_raw);
-    Barriers* bars = sm.bars;
+    uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* patches = ring + PRING_BYTES;
+    PairBars* bars = (PairBars*)(patches + NUM_EPI_WARPS * PATCH);
+    Plan& plan = *(Plan*)(bars + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int NT = (int)((NCOL + BN - 1) / BN);   // the last N-tile may run past NCOL: those columns are
-                                                  // products with zeros and never stored
-    const Sched sc = make_sched(csplit);
-    uint32_t tmem;
-    const int T = pipeline_setup(sm, offsets, E, R, NUM_EPI_THREADS, &tmem);
+    const int rank = (int)cluster_rank();
+    const int NT = (int)((NCOL + TILE - 1) / TILE);
+    const int sbytes = stage_bytes(most), stages = ring_stages(most);
+
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int64_t b, en;
+        expert_range(offsets, e, R, b, en);
+        plan.begin[e] = (int)b;
+        plan.rows[e] = (int)(en - b);
+        plan.start[e + 1] = (int)((en - b + most - 1) / most);
+    }
+    if (threadIdx.x == 0) plan.start[0] = 0;
+    __syncthreads();
+    if (warp == 0) prefix_in_place(plan.start, E, lane);
+    const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS);
+    const int jobs = plan.start[E] * NT;
+    const int j0 = blockIdx.x >> 1, jstep = gridDim.x >> 1;
 
     if (warp == 0) {
-        if (lane == 0)
-            run_producer(sm, sc, &map_a, offsets, E, R, T, NT, KB, status,
-                         [&](uint8_t* sb, int e, int nt, int kb, uint64_t* bar, uint64_t pol) {
-                             if constexpr (W_MN) {
-#pragma unroll
-                                 for (int j = 0; j < BN / 64; ++j)
-                                     tma_load_3d_hint(sb + j * BMN_BOX_BYTES, &map_w, nt * BN + 64 * j, kb * BK, e, bar, pol);
-                             } else {
-                                 tma_load_3d_hint(sb, &map_w, kb * BK, nt * BN, e, bar, pol);
-                             }
-                         });
-    } else if (warp == 1) {
-        if (lane == 0) run_mma<W_MN>(sm, sc, tmem, T, NT, KB, status);
-    } else {
-        const int quad = warp & 3;
-        const int slot = (warp - 2) >> 2;
-        const int lrow = quad * 32 + lane;
-        const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
-        uint8_t* stage = (uint8_t*)(((uintptr_t)sm.extra + 1023) & ~(uintptr_t)1023) + (warp - 2) * STAGE_TILE;
-        const bool bias_vec = ((uintptr_t)bias & 15) == 0;       // NCOL % 8 == 0 keeps every chunk of it aligned
-        bool stores_pending = false;             // lane 0 has TMA stores in flight
-        int job = 0;
+        // ------------------------------------------------ TMA producer (both CTAs; the warp converged, one lane issues)
+        const bool elected = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, pending = 0, pend_par = 0;
+        const uint64_t pol_w = make_policy<kHintB>(), pol_r = make_policy<kHintA>();
         bool ok = true;
-        // 32 columns of this lane's row as 16 bf16 pairs -> the warp's staged tile -> one TMA store
-        auto store_tile = [&](const CUtensorMap* map, const uint32_t (&w)[CW / 2], int col, int row) {
-            if (stores_pending) {
-                if (lane == 0) bulk_wait_read_all();
-                __syncwarp();
-            }
+        Job next = {};
+        if (j0 < jobs) next = job_at(j0, plan, E, NT);
+        for (int j = j0; ok && j < jobs; j += jstep) {
+            const Job q = next;
+            const int c0 = q.nt * TILE + rank * 128;
+            const uint32_t bytes = (uint32_t)(2 * PA_BYTES + q.n * 128);
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!pair_wait(&bars->empty[stage], phase ^ 1, &bars->abort, status)) { ok = false; break; }
+                if (elected) {
+                    if (rank == 0) mbar_expect_tx(&bars->full[stage], bytes);
+                    const uint32_t bar = cluster_addr(&bars->full[stage], 0);
+                    uint8_t* sa = ring + stage * sbytes;
+                    if constexpr (W_MN) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                st_shared_v4(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), w[4 * q], w[4 * q + 1], w[4 * q + 2],
-                             w[4 * q + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tma_store_2d(map, col, row, stage);
-                bulk_commit();
-            }
-            stores_pending = true;
-        };
-        // a job's 32-column chunks are dealt out over the EPW warps of a quadrant: slot, slot + EPW, ..
-        // This lane's residual of its next chunk (of this job or the next) is fetched while a chunk is
-        // worked off.
-        Vec<4> res[4];
-        auto fetch_residual = [&](int64_t row0, int64_t row_end, int64_t j0) {
-            if (row0 + lrow < row_end) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (j0 + 8 * q < NCOL)
-                        res[q] = ld_stream<4, true>((const Vec<4>*)(residual + (row0 + lrow) * NCOL + j0 + 8 * q));
-            }
-        };
-        int e = 0;
-        int64_t row0 = 0, row_end = 0;
-        if (sc.t0 < T) {
-            tile_rows(sm.tile_start, offsets, E, R, sc.t0, e, row0, row_end);
-            if (residual) fetch_residual(row0, row_end, (int64_t)sc.n0 * BN + slot * CW);
-        }
-        for (int t = sc.t0; t < T; t += sc.tstep) {
-            int e_next = e;
-            int64_t row0_next = row0, row_end_next = row_end;
-            if (t + sc.tstep < T) tile_rows(sm.tile_start, offsets, E, R, t + sc.tstep, e_next, row0_next, row_end_next);
-            const int64_t row = row0 + lrow;
-            const bool full_quad = row0 + quad * 32 + 31 < row_end;
-            for (int nt = sc.n0; nt < NT; nt += sc.nstep, ++job) {
-                const int acc = job & 1;
-                const bool last_job = nt + sc.nstep >= NT;            // of this M-tile
-                if (ok && !mbar_wait(&bars->tfull[acc], (uint32_t)((job >> 1) & 1), bars, status)) ok = false;
-                ok = __all_sync(FULL_MASK, ok);      // tcgen05.ld below is warp-collective
-                const bool valid = ok && row < row_end;
-                tc_fence_after();
-#pragma unroll 1
-                for (int k = slot; k < NCH; k += EPW) {
-                    const int64_t j0 = (int64_t)nt * BN + k * CW;
-                    const bool chunk = j0 < NCOL;                 // NCOL % 8 == 0: whole groups of 8
-                    const bool last = k + EPW >= NCH;
-                    float v[CW];
-                    if (ok) tc_ld<CW>(tmem + t_lane + (uint32_t)(acc * BN + k * CW), v);
-                    if (last) {
-                        tc_fence_before();
-                        mbar_arrive(&bars->tempty[acc]);          // the accumulator may be overwritten
+                        for (int i = 0; i < 2; ++i)
+                            pair_load_3d(sa + i * PBOX_BYTES, &map_w, c0 + 64 * i, kb * BK, q.e, bar, pol_w);
+                    } else {
+                        pair_load_3d(sa, &map_w, kb * BK, c0, q.e, bar, pol_w);
                     }
-                    if (bias && chunk) {
-                        // one address for the warp, 16 bytes where the bias allows
-                        const float* b = bias + (int64_t)e * NCOL + j0;
+                    const int half = q.n >> 1;                   // rows of this CTA: a multiple of 16
+                    int at = 0;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            if (j0 + 4 * q >= NCOL) continue;
-                            float4 f;
-                            if (bias_vec) f = __ldg((const float4*)(b + 4 * q));
-                            else f = make_float4(__ldg(b + 4 * q), __ldg(b + 4 * q + 1), __ldg(b + 4 * q + 2), __ldg(b + 4 * q + 3));
-                            v[4 * q] += f.x;
-                            v[4 * q + 1] += f.y;
-                            v[4 * q + 2] += f.z;
-                            v[4 * q + 3] += f.w;
+                    for (int i = 0; i < 4; ++i) {
+                        if (half & (128 >> i)) {
+                            pair_load_2d(sa + PA_BYTES + at * 128, &map_r.m[i], kb * BK, q.row0 + rank * half + at, bar, pol_r);
+                            at += 128 >> i;
                         }
-                    }
-                    uint32_t w[CW / 2];
-                    if (pre && ok && chunk) {
-#pragma unroll
-                        for (int i = 0; i < CW / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                        if (full_quad) {
-                            store_tile(&map_pre, w, (int)j0, (int)(row0 + quad * 32));
-                        } else if (valid) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (j0 + 8 * q < NCOL)
-                                    st_stream<4>((Vec<4>*)(pre + row * NCOL + j0 + 8 * q),
-                                                 Vec<4>{{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]}});
-                        }
-                    }
-                    if constexpr (ACT != SITU_ACT_NONE) {
-#pragma unroll
-                        for (int i = 0; i < CW; ++i) v[i] = act_value<ACT>(v[i]);
-                    }
-                    if (residual) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                v[8 * q + 2 * i] += bf16_lo(res[q].w[i]);      // columns past NCOL and rows past
-                                v[8 * q + 2 * i + 1] += bf16_hi(res[q].w[i]);  // the expert are not stored
-                            }
-                        }
-                        if (!last) fetch_residual(row0, row_end, j0 + EPW * CW);
-                        else if (!last_job) fetch_residual(row0, row_end, (int64_t)(nt + sc.nstep) * BN + slot * CW);
-                        else if (t + sc.tstep < T) fetch_residual(row0_next, row_end_next, (int64_t)sc.n0 * BN + slot * CW);
-                    }
-                    if (!ok || !chunk) continue;
-                    if (out_fp32) {
-                        if (valid) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                if (j0 + 4 * q < NCOL)
-                                    st_stream<4>((Vec<4>*)((float*)out + row * NCOL + j0 + 4 * q),
-                                                 Vec<4>{{__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                                         __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])}});
-                        }
-                        continue;
-                    }
-#pragma unroll
-                    for (int i = 0; i < CW / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                    if (full_quad) {
-                        store_tile(&map_out, w, (int)j0, (int)(row0 + quad * 32));
-                    } else if (valid) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (j0 + 8 * q < NCOL)
-                                st_stream<4>((Vec<4>*)((uint16_t*)out + row * NCOL + j0 + 8 * q),
-                                             Vec<4>{{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]}});
                     }
                 }
+                pending |= 1u << stage;
+                pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == stages) { stage = 0; phase ^= 1; }
+                if (kb == 0 && j + jstep < jobs) next = job_at(j + jstep, plan, E, NT);   // while these loads fly
             }
-            e = e_next;
-            row0 = row0_next;
-            row_end = row_end_next;
         }
-        if (lane == 0 && stores_pending) bulk_wait_all();   // every staged tile written
+        __syncwarp();
+        if (rank == 0) pair_drain(bars, pending, pend_par);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader; the warp converged, one lane issues)
+        if (rank == 0) {
+            const bool elected = elect_one();
+            int stage = 0, job = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            int n_next = j0 < jobs ? job_at(j0, plan, E, NT).n : 0;
+            const uint32_t ring_addr = smem_addr(ring);
+            for (int j = j0; ok && j < jobs; j += jstep, ++job) {
+                const uint32_t idesc = pair_idesc(n_next, W_MN, false);
+                const int acc = job & 1;
+                const uint32_t d = tmem + (uint32_t)(acc * 256);
+                if (!pair_wait<true>(&bars->tempty[acc], (uint32_t)((job >> 1) & 1) ^ 1, &bars->abort, status)) break;
+                tc_fence_after();
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!pair_wait(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sa = ring_addr + (uint32_t)(stage * sbytes);
+                    const uint64_t ad = W_MN ? smem_desc_mn(sa) : smem_desc(sa), bd = smem_desc(sa + PA_BYTES);
+                    if (elected) {
+#pragma unroll
+                        for (int kk = 0; kk < BK / UK; ++kk)     // 16 deep: 32 bytes along a row, 2048 bytes MN-major
+                            pair_mma(d, ad + (uint64_t)(kk * (W_MN ? 128 : 2)), bd + (uint64_t)(kk * 2), idesc,
+                                     kk > 0 ? 1u : (uint32_t)kb);
+                        pair_commit(&bars->empty[stage]);
+                    }
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
+                    if (kb == 0 && j + jstep < jobs) n_next = job_at(j + jstep, plan, E, NT).n;   // while these run
+                }
+                if (ok && elected) pair_commit(&bars->tfull[acc]);
+            }
+            __syncwarp();
+            if (elected) pair_commit(&bars->mma_done);
+        }
+    } else {
+        // ------------------------------------------------ epilogue (both CTAs)
+        const int quad = warp & 3;
+        const int slot = (warp - 2) >> 2;
+        const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
+        uint8_t* patch = patches + (warp - 2) * PATCH;
+        const uint32_t patch_addr = smem_addr(patch);
+        int job = 0;
+        for (int j = j0; j < jobs; j += jstep, ++job) {
+            const Job q = job_at(j, plan, E, NT);
+            const int64_t col = (int64_t)q.nt * TILE + rank * 128 + quad * 32;   // the warp's 32 columns
+            const int ncols = (int)max((int64_t)0, min((int64_t)32, NCOL - col));
+            float b[4];                                          // bias of this lane's columns: lane / 4 + 8 i
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = (lane >> 2) + 8 * i;
+                b[i] = bias && c < ncols ? __ldg(bias + (int64_t)q.e * NCOL + col + c) : 0.0f;
+            }
+            const int acc = job & 1;
+            // residual pieces of the next patch, fetched a patch ahead
+            Vec<4> res[4];
+            auto fetch_residual = [&](int c) {
+                if (residual && ncols > 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = c + (lane >> 2) + 8 * i;
+                        if (r < q.rows && (lane & 3) * 8 < ncols)
+                            res[i] = ld_stream<4, true>((const Vec<4>*)(residual + (int64_t)(q.row0 + r) * NCOL + col + (lane & 3) * 8));
+                    }
+                }
+            };
+            fetch_residual(slot * CW);
+            const bool ok = pair_wait_epilogue(&bars->tfull[acc], (uint32_t)((job >> 1) & 1), bars, status, NUM_EPI_WARPS);
+#pragma unroll 1
+            for (int c = slot * CW; c < q.rows; c += EPW * CW) {
+                if (!ok) break;
+                const int left = q.rows - c;                   // uniform over the warp
+                const int64_t at = (int64_t)(q.row0 + c) * NCOL + col;
+                uint32_t v[2][16];                           // [columns 0-15, 16-31][8 rows: column l / 4 rows 2(l % 4), +1;
+                                                             //  column l / 4 + 8 the same]
+                tc_ld_16x256(tmem + t_lane + (uint32_t)(acc * 256 + c), v[0]);
+                tc_ld_16x256(tmem + t_lane + (16u << 16) + (uint32_t)(acc * 256 + c), v[1]);
+                if (residual) {
+                    __syncwarp();                            // the patch has been read out
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *(uint4*)(patch + patch_at((lane >> 2) + 8 * i, lane & 3)) = make_uint4(res[i].w[0], res[i].w[1], res[i].w[2], res[i].w[3]);
+                    __syncwarp();
+                    fetch_residual(c + EPW * CW);
+                }
+                tc_wait_ld();
+                float z[4][8];                               // [8-row group][column block 2: 0, 8, 16, 24][2 rows]
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[g][i] = __uint_as_float(v[i >> 2][4 * g + (i & 3)]) + b[i >> 1];
+                if (pre) {
+                    __syncwarp();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t r[4];
+                        if (residual) ld_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), r);
+                        __syncwarp();
+                        st_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), pack_bf16x2(z[g][0], z[g][1]),
+                                    pack_bf16x2(z[g][2], z[g][3]), pack_bf16x2(z[g][4], z[g][5]), pack_bf16x2(z[g][6], z[g][7]));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            z[g][i] = act_value<ACT>(z[g][i]);
+                            if (residual) z[g][i] += i & 1 ? bf16_hi(r[i >> 1]) : bf16_lo(r[i >> 1]);
+                        }
+                    }
+                    __syncwarp();
+                    patch_out(patch, pre, at, NCOL, left, ncols, lane);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t r[4];
+                        if (residual) ld_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), r);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            z[g][i] = act_value<ACT>(z[g][i]);
+                            if (residual) z[g][i] += i & 1 ? bf16_hi(r[i >> 1]) : bf16_lo(r[i >> 1]);
+                        }
+                    }
+                }
+                if (out_fp32) {                              // 8 lanes' columns of a row: 32 bytes
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 8 * g + 2 * (lane & 3) + (i & 1), cc = (lane >> 2) + 8 * (i >> 1);
+                            if (r < left && cc < ncols) ((float*)out)[at + (int64_t)r * NCOL + cc] = z[g][i];
+                        }
+                } else {
+                    __syncwarp();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        st_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), pack_bf16x2(z[g][0], z[g][1]),
+                                    pack_bf16x2(z[g][2], z[g][3]), pack_bf16x2(z[g][4], z[g][5]), pack_bf16x2(z[g][6], z[g][7]));
+                    __syncwarp();
+                    patch_out(patch, (uint16_t*)out, at, NCOL, left, ncols, lane);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars->tempty[acc], 0));   // read: may be overwritten
+        }
     }
-    pipeline_teardown(tmem);
+    pair_teardown(tmem, bars);
 }
 
 // ---------------------------------------------------------------- few rows per expert
@@ -229,8 +370,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // A decoding step gives an expert a row or a few: the product is a read of the weights (22 MB an
 // expert at 3584 x 3072), so the kernel is built around that read. A job is 16 weight rows (output
 // columns) and up to FEW_ROWS rows of one expert; the FEW_WARPS warps of a block share the
-// contraction (warp w takes every FEW_WARPS-th 64-wide block), each with its 16-byte loads of
-// FEW_U blocks in flight, and meet in shared memory at the end. The products run on mma.m16n8k16
+// contraction (warp w takes every FEW_WARPS-th 128-wide block), each with its block's 16-byte loads in
+// flight, and meet in shared memory at the end. The products run on mma.m16n8k16
 // with the weight rows as the 16 and the tokens as the 8 (a 128-row tcgen05 tile would be nearly
 // empty): the contraction's order is free, so a lane's 16-byte load of weights and the one of the
 // token's row at the same place are used as they come, as the fragments of two steps.
@@ -372,27 +513,31 @@ __global__ void __launch_bounds__(FEW_WARPS * 32)
 constexpr int64_t FEW_MAX_MEAN_ROWS = 8;
 constexpr int64_t FEW_MAX_DENSE_ROWS = 64;
 
-int check_linear(int64_t E, const void* offsets, int64_t R, int64_t N, int64_t K) {
-    if (R < 0 || R > INT32_MAX || N < 8 || N % 8 != 0 || K < 8 || K % 8 != 0 || E < 1 || E > MAX_EXPERTS)
-        return SITU_GLU_INVALID_ARG;
-    if (N > INT32_MAX / 4 || K > INT32_MAX / 4 || E * N > INT32_MAX || E * K > INT32_MAX) return SITU_GLU_INVALID_ARG;
-    if (!offsets && E != 1) return SITU_GLU_INVALID_ARG;
-    return SITU_GLU_OK;
+// Most rows per job. A job of n rows takes a 64-deep block in the larger of 2n cycles (tensor cores) and the time
+// its (256 + n)·64 bytes per SM need at ~50 bytes a cycle (measured), and jobs run in rounds over the pairs of
+// SMs: 256 rows for large shapes, less where that would leave pairs without a job or a round mostly empty.
+// 4096 x 3584 x 3584 takes 256 rows (3 rounds), 256 x 3584 x 3584 takes 64 (56 jobs).
+int64_t block_cycles(int64_t n) {
+    const int64_t bytes = (256 + n) * 64 / 50;
+    return 2 * n > bytes ? 2 * n : bytes;
 }
 
-// CTAs sharing an M-tile (its N-tiles dealt out among them): of 4 .. 16, the fewest job rounds for the
-// M-tiles expected; more CTAs on a tile at equal rounds keep fewer A tiles live in L2.
-int pick_csplit(int64_t R, int64_t E, int NT, int sms) {
-    const int64_t tiles = (R + BM - 1) / BM + (E > 1 ? E / 2 : 0);
-    int best = NT < 4 ? NT : 4;
+int pick_chunk(int64_t R, int64_t E, int NT, int64_t KB, int pairs) {
+    const int64_t rows = (R + E - 1) / E;    // of an expert, on average
+    int best = MAX_CHUNK;
     int64_t best_cost = INT64_MAX;
-    for (int c = best; c <= NT && c <= 16; ++c) {
-        const int groups = sms / c;
-        if (groups < 1) break;
-        const int64_t cost = ((tiles + groups - 1) / groups) * ((NT + c - 1) / c);
-        if (cost <= best_cost) {
+    for (int most = MAX_CHUNK; most >= 32; most -= 32) {
+        const int64_t chunks = (rows + most - 1) / most, n = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
+        const int64_t last = (rows - (chunks - 1) * n + 31) / 32 * 32;       // the last chunk's, computed last
+        const int64_t full = E * (last < n ? chunks - 1 : chunks) * NT, part = last < n ? E * NT : 0;
+        const int64_t rounds = (full + pairs - 1) / pairs, left = rounds * pairs - full;
+        const int64_t more = part > left ? (part - left + pairs - 1) / pairs : 0;
+        const int64_t each = KB * block_cycles(n) + 4 * n + 1500, tail = KB * block_cycles(last) + 4 * last + 1500;
+        // many rounds even out over ragged experts; few do not
+        const int64_t cost = rounds >= 16 ? (full * each + part * tail) / pairs : rounds * each + more * tail;
+        if (cost < best_cost) {
             best_cost = cost;
-            best = c;
+            best = most;
         }
     }
     return best;
@@ -401,34 +546,28 @@ int pick_csplit(int64_t R, int64_t E, int NT, int sms) {
 template <bool W_MN, int ACT>
 int launch_tc(const void* a, const void* w, const int64_t* offsets, int64_t E, const float* bias, const void* residual,
               void* out, bool out_fp32, void* pre, int* status, int64_t R, int64_t NCOL, int64_t KC, cudaStream_t stream) {
-    CUtensorMap map_a, map_w, map_out = {}, map_pre = {};
-    if (!make_map(&map_a, a, (uint64_t)R, (uint64_t)KC, BM)) return cuda_fail(cudaErrorInvalidValue);
+    CUtensorMap map_w;
+    RowMaps map_r;
+    for (int i = 0; i < 4; ++i)
+        if (!make_map(&map_r.m[i], a, (uint64_t)R, (uint64_t)KC, 128u >> i)) return cuda_fail(cudaErrorInvalidValue);
     // [E, N, K] as stored; forward: contraction K innermost, dgrad: output columns K innermost
     const uint64_t inner = (uint64_t)(W_MN ? NCOL : KC), rows = (uint64_t)(W_MN ? KC : NCOL);
     const uint64_t dims[3] = {inner, rows, (uint64_t)E}, strides[2] = {inner * 2, inner * rows * 2};
-    const uint32_t box[3] = {64, W_MN ? (uint32_t)BK : (uint32_t)BN, 1};
+    const uint32_t box[3] = {64, W_MN ? (uint32_t)BK : 128u, 1};
     if (!make_map_any(&map_w, w, false, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
         return cuda_fail(cudaErrorInvalidValue);
-    const uint64_t od[2] = {(uint64_t)NCOL, (uint64_t)R}, os[1] = {(uint64_t)NCOL * 2};
-    const uint32_t ob[2] = {CW, 32};
-    if (!out_fp32 && !make_map_any(&map_out, out, false, 2, od, os, ob, CU_TENSOR_MAP_SWIZZLE_64B))
-        return cuda_fail(cudaErrorInvalidValue);
-    if (pre && !make_map_any(&map_pre, pre, false, 2, od, os, ob, CU_TENSOR_MAP_SWIZZLE_64B))
-        return cuda_fail(cudaErrorInvalidValue);
-    auto kernel = linear_tc_kernel<W_MN, ACT>;
-    cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) return cuda_fail(e);
-    int dev = 0, sms = 0, grid = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return cuda_fail(e);
-    const int csplit = pick_csplit(R, E, (int)((NCOL + BN - 1) / BN), sms);
-    if ((e = (cudaError_t)persistent_grid(R, E, csplit, &grid)) != cudaSuccess) return cuda_fail(e);
-    kernel<<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(map_a, map_w, map_out, map_pre, offsets, bias,
-                                                      (const uint16_t*)residual, out, out_fp32 ? 1 : 0, (uint16_t*)pre,
-                                                      status, (int)E, R, NCOL, (int)((KC + BK - 1) / BK), csplit);
-    e = cudaGetLastError();
+    int sms = 0;
+    const int st = sm_count(&sms);
+    if (st != SITU_GLU_OK) return st;
+    const int NT = (int)((NCOL + TILE - 1) / TILE);
+    const int64_t KB = (KC + BK - 1) / BK;
+    const int most = pick_chunk(R, E, NT, KB, sms / 2);
+    const int64_t jobs = ((R + most - 1) / most + E - 1) * NT;   // at most: every expert's last chunk partial
+    if (jobs > INT32_MAX - 2 * sms) return SITU_GLU_INVALID_ARG;  // the kernel counts them in 32 bits
+    const cudaError_t e = launch_pairs(linear_tc_kernel<W_MN, ACT>, jobs, NUM_THREADS, SMEM_BYTES, stream, map_w, map_r,
+                                       offsets, bias, (const uint16_t*)residual, out, out_fp32 ? 1 : 0, (uint16_t*)pre,
+                                       status, (int)E, R, NCOL, (int)KB, most);
     return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
 }
 

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/situ_moe.h"
+#include "situ_host.h"
 
 namespace situ_linear {
 
@@ -72,6 +73,24 @@ __device__ __forceinline__ void prefix_in_place(int* start, int E, int lane) {
         run += start[i];
         start[i] = run;
     }
+}
+
+// ---------------------------------------------------------------- host side
+
+inline int sm_count(int* sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    return e == cudaSuccess ? SITU_GLU_OK : situ_host::cuda_fail(e);
+}
+
+// Sizes shared by the product and its gradients.
+inline int check_linear(int64_t E, const void* offsets, int64_t R, int64_t N, int64_t K) {
+    if (R < 0 || R > INT32_MAX || N < 8 || N % 8 != 0 || K < 8 || K % 8 != 0 || E < 1 || E > SITU_MAX_EXPERTS)
+        return SITU_GLU_INVALID_ARG;
+    if (N > INT32_MAX / 4 || K > INT32_MAX / 4 || E * N > INT32_MAX || E * K > INT32_MAX) return SITU_GLU_INVALID_ARG;
+    if (!offsets && E != 1) return SITU_GLU_INVALID_ARG;
+    return SITU_GLU_OK;
 }
 
 }  // namespace situ_linear

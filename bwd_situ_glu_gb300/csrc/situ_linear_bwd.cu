@@ -395,20 +395,6 @@ int64_t wgrad_splits(int64_t R, int64_t N, int64_t K, int64_t E) {
     return s < 1 ? 1 : s;
 }
 
-int check_linear(int64_t E, const void* offsets, int64_t R, int64_t N, int64_t K) {
-    if (R < 0 || R > INT32_MAX || N < 8 || N % 8 != 0 || K < 8 || K % 8 != 0 || E < 1 || E > MAX_EXPERTS)
-        return SITU_GLU_INVALID_ARG;
-    if (N > INT32_MAX / 4 || K > INT32_MAX / 4 || E * N > INT32_MAX || E * K > INT32_MAX) return SITU_GLU_INVALID_ARG;
-    if (!offsets && E != 1) return SITU_GLU_INVALID_ARG;
-    return SITU_GLU_OK;
-}
-
-int sm_count(int* sms) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
-}
 
 }  // namespace
 
