@@ -12,13 +12,13 @@
 #include "situ_device.cuh"
 #include "situ_host.h"
 #include "situ_linear.cuh"
-#include "situ_tc.cuh"
+#include "situ_pair.cuh"
 
 namespace {
 
 using namespace situ;
 using namespace situ_host;
-using namespace situ_tc;
+using namespace situ_pair;
 using namespace situ_linear;
 
 // ---------------------------------------------------------------- dz and the bias gradient
@@ -137,50 +137,58 @@ __global__ void __launch_bounds__(BIAS_COLS)
 
 // ---------------------------------------------------------------- the weight gradient
 
-// dW_e [N, K] = dz_eᵀ·a_e on the tensor cores. A job is a 128 x 256 tile of one expert's dW; its
-// contraction runs over the expert's rows, 64 to a ring stage. Both operands are read as they are
-// stored, rows apart ("MN-major": per stage two 64-column boxes of dz, four of a, 128-byte swizzle).
-// A TMA box cannot end at an expert's last row, so the last stage brings rows of the next expert (or
-// zeros past the tensor): the MMA warp issues only the 16-row steps that hold rows of the expert and
-// first zeroes, in both operands, the rows past its end in the last step (generic-proxy writes, then
-// the proxy fence), so nothing of another expert enters, NaN included.
+// dW_e [N, K] = dz_eᵀ·a_e on the tensor cores, on pairs of SMs (situ_pair.cuh). A job is a 256 x 256 tile of one
+// expert's dW; its contraction runs over the expert's rows, 64 to a ring stage. Both operands are read as they
+// are stored, rows apart ("MN-major": per stage and CTA two 64-column boxes of dz and two of a, 128-byte swizzle).
+//
+// A TMA box cannot end at an expert's last row, so its last stage brings rows of the next expert (or zeros past
+// the tensor). Only the 16-row steps that hold rows of the expert are issued, and where the last of them is
+// partial both CTAs first zero the rows past the end, in both operands (generic-proxy writes, the proxy fence, an
+// arrival at the leader's tail_ready), so nothing of another expert enters, NaN included. Such a stage's
+// loads count at the CTA's own tail_full barrier of that stage, since each CTA must see its own (one barrier a stage:
+// experts of a few rows have several ragged stages in the ring).
 //
 // The tensor cores cut each step's fp32 sum towards zero, an error that grows with the steps (measured
 // against float64 at 2048 x 2048: 5e-7 of the norm after 512 rows, 4.4e-6 after 4096, 1.9e-5 after
 // 16384). dW feeds an fp32 optimizer, so an accumulator takes at most CHUNK_BLOCKS stages (512 rows)
 // and the epilogue's threads add the chunks in registers, rounded to nearest, while the tensor cores
-// fill the other accumulator. Where the tiles of dW cannot
-// fill the SMs, the rows are cut into `splits` pieces whose sums (fp32, in the workspace) a second
-// kernel adds in order.
+// fill the other accumulator. Where the tiles of dW cannot fill the SMs, the rows are cut into `splits` pieces
+// whose sums (fp32, in the workspace) a second kernel adds in order.
 constexpr int CHUNK_BLOCKS = 8;
 constexpr int EPW = 2;
-constexpr int NUM_EPI_THREADS = 4 * EPW * 32;
-constexpr int NUM_THREADS = 64 + NUM_EPI_THREADS;
+constexpr int NUM_EPI_WARPS = 4 * EPW;
+constexpr int NUM_THREADS = 64 + NUM_EPI_WARPS * 32;
+constexpr int TILE = 256;
 constexpr int STAGE_TILE = 32 * 128;         // 32 rows x 128 bytes of dW
-constexpr int BOX_BYTES = 64 * BK * 2;       // 64 columns x 64 rows
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 4 * EPW * STAGE_TILE + (int)sizeof(Barriers);
+constexpr int SBYTES = PA_BYTES + PB_BYTES;
+constexpr int STAGES_W = 5;
+static_assert(STAGES_W <= PSTAGES, "ring barriers");
+
+struct WPlan {
+    int begin[MAX_EXPERTS];                  // first row and rows of each expert
+    int rows[MAX_EXPERTS];
+};
+constexpr int SMEM_BYTES = 1024 + STAGES_W * SBYTES + NUM_EPI_WARPS * STAGE_TILE + (int)sizeof(PairBars) + (int)sizeof(WPlan);
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
 struct WJob {
-    int e, mt, nt, plane;
-    int64_t row0, rows;                      // rows to contract over
+    int mt, nt, plane;
+    int row0, rows;                          // rows to contract over
 };
 
-__device__ __forceinline__ WJob wgrad_job(int64_t j, const int64_t* offsets, int E, int64_t R, int MT, int NT,
-                                          int splits) {
+// Job j: experts, then pieces of their rows, then tiles of dW. 32-bit: the host bounds their number.
+__device__ __forceinline__ WJob wgrad_job(int j, const WPlan& plan, int E, int MT, int NT, int splits) {
     WJob w;
-    w.nt = (int)(j % NT);
-    j /= NT;
-    w.mt = (int)(j % MT);
-    j /= MT;
-    const int s = (int)(j % splits);
-    w.e = (int)(j / splits);
-    w.plane = s * E + w.e;
-    int64_t b, en;
-    expert_range(offsets, w.e, R, b, en);
-    const int64_t blocks = (en - b + BK - 1) / BK, per = (blocks + splits - 1) / splits;
-    w.row0 = min(en, b + s * per * BK);
-    w.rows = min(en, w.row0 + per * BK) - w.row0;
+    const int jm = j / NT;
+    w.nt = j - jm * NT;
+    const int js = jm / MT;
+    w.mt = jm - js * MT;
+    const int e = js / splits, s = js - e * splits;
+    w.plane = s * E + e;
+    const int rows = plan.rows[e];
+    const int piece = ((rows + BK - 1) / BK + splits - 1) / splits * BK;
+    w.row0 = plan.begin[e] + min(rows, s * piece);
+    w.rows = min(rows, (s + 1) * piece) - min(rows, s * piece);
     return w;
 }
 
@@ -192,148 +200,170 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                  int* __restrict__ status, int E, int64_t R, int64_t N, int64_t K, int MT, int NT, int splits) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* staging = ring + STAGES * STAGE_BYTES;
-    Barriers* bars = (Barriers*)(staging + 4 * EPW * STAGE_TILE);
+    uint8_t* staging = ring + STAGES_W * SBYTES;
+    PairBars* bars = (PairBars*)(staging + NUM_EPI_WARPS * STAGE_TILE);
+    WPlan& plan = *(WPlan*)(bars + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t jobs = (int64_t)E * splits * MT * NT;
+    const int rank = (int)cluster_rank();
+    const int jobs = E * splits * MT * NT;
+    const int j0 = blockIdx.x >> 1, jstep = gridDim.x >> 1;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
-        }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(&bars->tfull[a], 1);
-            mbar_init(&bars->tempty[a], NUM_EPI_THREADS);
-        }
-        mbar_init(&bars->mma_done, 1);
-        bars->abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int64_t b, en;
+        expert_range(offsets, e, R, b, en);
+        plan.begin[e] = (int)b;
+        plan.rows[e] = (int)(en - b);
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars->tmem_base)),
-                     "r"(TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS);
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, pending = 0, pend_par = 0;
-            const uint64_t pol = make_policy<L2Hint::normal>();
-            bool ok = true;
-            for (int64_t j = blockIdx.x; ok && j < jobs; j += gridDim.x) {
-                const WJob w = wgrad_job(j, offsets, E, R, MT, NT, splits);
-                const int kbs = (int)((w.rows + BK - 1) / BK);
-                for (int kb = 0; kb < kbs; ++kb) {
-                    if (!mbar_wait(&bars->empty[stage], phase ^ 1, bars, status)) { ok = false; break; }
-                    mbar_expect_tx(&bars->full[stage], STAGE_BYTES);
-                    uint8_t* sa = ring + stage * STAGE_BYTES;
-                    const int row = (int)(w.row0 + (int64_t)kb * BK);
-#pragma unroll
-                    for (int i = 0; i < BM / 64; ++i)
-                        tma_load_2d_hint(sa + i * BOX_BYTES, &map_dz, w.mt * BM + 64 * i, row, &bars->full[stage], pol);
-#pragma unroll
-                    for (int i = 0; i < BN / 64; ++i)
-                        tma_load_2d_hint(sa + A_BYTES + i * BOX_BYTES, &map_a, w.nt * BN + 64 * i, row, &bars->full[stage], pol);
-                    pending |= 1u << stage;
-                    pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
-                }
-            }
-            for (int s = 0; s < STAGES; ++s)
-                if (pending & (1u << s)) mbar_drain(&bars->full[s], (pend_par >> s) & 1u);
-        }
-    } else if (warp == 1) {
-        // the whole warp walks the stages (it zeroes the rows past an expert's end); lane 0 issues
-        int stage = 0, done = 0;
-        uint32_t phase = 0;
+        // ------------------------------------------------ TMA producer (both CTAs; the warp converged, one lane issues)
+        const bool elected = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, pending = 0, pend_par = 0;
+        uint32_t tail_used = 0, tail_next = 0;                   // bit s: stage s held a ragged stage; the next one's parity
+        const uint64_t pol = make_policy<L2Hint::normal>();
         bool ok = true;
-        for (int64_t j = blockIdx.x; ok && j < jobs; j += gridDim.x) {
-            const WJob w = wgrad_job(j, offsets, E, R, MT, NT, splits);
-            const int kbs = (int)((w.rows + BK - 1) / BK);
-            for (int kb = 0; ok && kb < kbs; ++kb) {
-                const int acc = done & 1, in_chunk = kb % CHUNK_BLOCKS;
-                const bool chunk_ends = in_chunk + 1 == CHUNK_BLOCKS || kb + 1 == kbs;
-                const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
-                if (in_chunk == 0) {
-                    ok = __all_sync(FULL_MASK, mbar_wait(&bars->tempty[acc], (uint32_t)((done >> 1) & 1) ^ 1, bars, status));
-                    if (!ok) break;
+        WJob next = wgrad_job(j0, plan, E, MT, NT, splits);
+        for (int j = j0; ok && j < jobs; j += jstep) {
+            const WJob w = next;
+            const int kbs = (w.rows + BK - 1) / BK;
+            const bool ragged = (w.rows & (UK - 1)) != 0;
+            const int ca = w.mt * TILE + rank * 128, cb = w.nt * TILE + rank * 128;
+            if (kbs == 0 && j + jstep < jobs) next = wgrad_job(j + jstep, plan, E, MT, NT, splits);
+            for (int kb = 0; kb < kbs; ++kb) {
+                if (!pair_wait(&bars->empty[stage], phase ^ 1, &bars->abort, status)) { ok = false; break; }
+                if (elected) {
+                    uint8_t* sa = ring + stage * SBYTES;
+                    const int row = w.row0 + kb * BK;
+                    uint32_t bar;
+                    if (ragged && kb + 1 == kbs) {
+                        if (rank == 0) mbar_arrive(&bars->full[stage]);
+                        mbar_expect_tx(&bars->tail_full[stage], SBYTES);
+                        bar = smem_addr(&bars->tail_full[stage]);
+                    } else {
+                        if (rank == 0) mbar_expect_tx(&bars->full[stage], 2 * SBYTES);
+                        bar = cluster_addr(&bars->full[stage], 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        pair_load_2d(sa + i * PBOX_BYTES, &map_dz, ca + 64 * i, row, bar, pol);
+                        pair_load_2d(sa + PA_BYTES + i * PBOX_BYTES, &map_a, cb + 64 * i, row, bar, pol);
+                    }
                 }
-                ok = __all_sync(FULL_MASK, mbar_wait(&bars->full[stage], phase, bars, status));
-                if (!ok) break;
-                uint8_t* sa = ring + stage * STAGE_BYTES;
-                const int valid = (int)min((int64_t)BK, w.rows - (int64_t)kb * BK);
-                const int steps = (valid + UK - 1) / UK;
-                if (valid < steps * UK) {
-                    const int n16 = (steps * UK - valid) * 8;          // 16-byte pieces per box
-                    for (int i = lane; i < n16 * (STAGE_BYTES / BOX_BYTES); i += 32) {
+                if (ragged && kb + 1 == kbs) {
+                    tail_used |= 1u << stage;
+                    tail_next ^= 1u << stage;
+                }
+                pending |= 1u << stage;
+                pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES_W) { stage = 0; phase ^= 1; }
+                if (kb == 0 && j + jstep < jobs) next = wgrad_job(j + jstep, plan, E, MT, NT, splits);   // while these fly
+            }
+        }
+        __syncwarp();
+        if (rank == 0) pair_drain(bars, pending, pend_par);
+        for (int s = 0; s < STAGES_W; ++s)
+            if (tail_used >> s & 1) mbar_drain(&bars->tail_full[s], (tail_next >> s & 1) ^ 1);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader); zeroing of ragged tails (both CTAs)
+        const bool elected = elect_one();
+        int stage = 0, done = 0;
+        uint32_t phase = 0, tails = 0;                           // bit s of tails: parity of stage s's ragged uses
+        bool ok = true;
+        const uint32_t idesc = pair_idesc(TILE, true, true);
+        const uint32_t ring_addr = smem_addr(ring);
+        WJob next = wgrad_job(j0, plan, E, MT, NT, splits);
+        for (int j = j0; ok && j < jobs; j += jstep) {
+            const int rows = next.rows;
+            const int kbs = (rows + BK - 1) / BK;
+            if (j + jstep < jobs && (kbs == 0 || rank != 0)) next = wgrad_job(j + jstep, plan, E, MT, NT, splits);
+            if (rank != 0) {                                     // only the ragged stage of a job concerns this CTA
+                stage = (stage + kbs) % STAGES_W;
+                if ((rows & (UK - 1)) == 0) continue;
+            }
+            for (int kb = rank == 0 ? 0 : kbs - 1; kb < kbs; ++kb) {
+                const int valid = min(BK, rows - kb * BK), steps = (valid + UK - 1) / UK;
+                const int in_chunk = kb % CHUNK_BLOCKS, acc = done & 1;
+                const bool chunk_ends = in_chunk + 1 == CHUNK_BLOCKS || kb + 1 == kbs;
+                const int st = rank == 0 ? stage : (stage + STAGES_W - 1) % STAGES_W;
+                if (rank == 0) {
+                    if (in_chunk == 0) ok = pair_wait<true>(&bars->tempty[acc], (uint32_t)((done >> 1) & 1) ^ 1, &bars->abort, status);
+                    if (ok) ok = pair_wait(&bars->full[st], phase, &bars->abort, status);
+                }
+                if (ok && (valid & (UK - 1))) {                  // the job's last stage, its last step partial
+                    ok = pair_wait(&bars->tail_full[st], tails >> st & 1, &bars->abort, status);
+                    if (!ok) break;
+                    uint8_t* sa = ring + st * SBYTES;
+                    const int n16 = (steps * UK - valid) * 8;    // 16-byte pieces per box
+                    for (int i = lane; i < n16 * (SBYTES / PBOX_BYTES); i += 32) {
                         const int box = i / n16;
-                        st_shared_v4(sa + box * BOX_BYTES + valid * 128 + (i - box * n16) * 16, 0, 0, 0, 0);
+                        st_shared_v4(sa + box * PBOX_BYTES + valid * 128 + (i - box * n16) * 16, 0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars->tail_ready[st], 0));
+                    if (rank == 0) ok = pair_wait<true>(&bars->tail_ready[st], tails >> st & 1, &bars->abort, status);
+                    tails ^= 1u << st;
                 }
+                if (!ok) break;
+                if (rank != 0) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t ad = smem_desc_mn(smem_addr(sa)), bd = smem_desc_mn(smem_addr(sa + A_BYTES));
-                    for (int kk = 0; kk < steps; ++kk)   // 16 rows = 2048 bytes further (128 descriptor units)
-                        tc_mma_abmn(d_tmem, ad + (uint64_t)(kk * 128), bd + (uint64_t)(kk * 128), (in_chunk > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit(&bars->empty[stage]);
-                    if (chunk_ends) tc_commit(&bars->tfull[acc]);
+                const uint32_t d = tmem + (uint32_t)(acc * 256), sa = ring_addr + (uint32_t)(st * SBYTES);
+                const uint64_t ad = smem_desc_mn(sa), bd = smem_desc_mn(sa + PA_BYTES);
+                if (elected) {
+#pragma unroll
+                    for (int kk = 0; kk < BK / UK; ++kk)         // 16 rows = 2048 bytes further (128 descriptor units)
+                        if (kk < steps)
+                            pair_mma(d, ad + (uint64_t)(kk * 128), bd + (uint64_t)(kk * 128), idesc,
+                                     kk > 0 ? 1u : (uint32_t)in_chunk);
+                    pair_commit(&bars->empty[st]);
+                    if (chunk_ends) pair_commit(&bars->tfull[acc]);
                 }
-                __syncwarp();
                 done += chunk_ends;
-                if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                if (++stage == STAGES_W) { stage = 0; phase ^= 1; }
+                if (kb == 0 && j + jstep < jobs) next = wgrad_job(j + jstep, plan, E, MT, NT, splits);   // while these run
             }
         }
-        if (lane == 0) {
-            tc_commit(&bars->mma_done);
-            mbar_drain(&bars->mma_done, 0);
-        }
         __syncwarp();
+        if (rank == 0 && elected) pair_commit(&bars->mma_done);
     } else {
+        // ------------------------------------------------ epilogue (both CTAs): a lane holds one row of dW
         const int quad = warp & 3;
         const int slot = (warp - 2) >> 2;
         const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
         uint8_t* stage = staging + (warp - 2) * STAGE_TILE;
-        constexpr int COLS = BN / EPW;               // columns of this warp
+        constexpr int COLS = TILE / EPW;             // columns of this warp
         constexpr int CW = OUT_FP32 ? 32 : 64;       // columns per 128-byte staged row
         bool stores_pending = false;
-        bool ok = true;
         int done = 0;
-        for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
-            const WJob w = wgrad_job(j, offsets, E, R, MT, NT, splits);
-            const int chunks = (int)((w.rows + CHUNK_BLOCKS * BK - 1) / (CHUNK_BLOCKS * BK));
+        for (int j = j0; j < jobs; j += jstep) {
+            const WJob w = wgrad_job(j, plan, E, MT, NT, splits);
+            const int chunks = (w.rows + CHUNK_BLOCKS * BK - 1) / (CHUNK_BLOCKS * BK);
+            bool ok = true;
             float sum[COLS];
 #pragma unroll
             for (int i = 0; i < COLS; ++i) sum[i] = 0.0f;
             for (int ch = 0; ch < chunks; ++ch, ++done) {
                 const int acc = done & 1;
-                if (ok && !mbar_wait(&bars->tfull[acc], (uint32_t)((done >> 1) & 1), bars, status)) ok = false;
-                ok = __all_sync(FULL_MASK, ok);
-                tc_fence_after();
+                ok = pair_wait_epilogue(&bars->tfull[acc], (uint32_t)((done >> 1) & 1), bars, status, NUM_EPI_WARPS);
                 if (ok) {
 #pragma unroll
-                    for (int h = 0; h < COLS; h += 32) {
-                        float v[32];
-                        tc_ld<32>(tmem + t_lane + (uint32_t)(acc * BN + slot * COLS + h), v);
+                    for (int h = 0; h < COLS; h += 16) {
+                        float v[16];
+                        tc_ld<16>(tmem + t_lane + (uint32_t)(acc * 256 + slot * COLS + h), v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[h + i] += v[i];
+                        for (int i = 0; i < 16; ++i) sum[h + i] += v[i];
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&bars->tempty[acc]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars->tempty[acc], 0));
             }
-            const int n0 = w.mt * BM + quad * 32;
+            const int n0 = w.mt * TILE + rank * 128 + quad * 32;
 #pragma unroll
             for (int c = 0; c < COLS; c += CW) {
-                const int col = w.nt * BN + slot * COLS + c;
+                const int col = w.nt * TILE + slot * COLS + c;
                 if (!ok || n0 >= N || col >= K) continue;      // uniform over the warp
                 if (stores_pending) {
                     if (lane == 0) bulk_wait_read_all();
@@ -363,7 +393,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (lane == 0 && stores_pending) bulk_wait_all();
     }
-    pipeline_teardown(tmem);
+    pair_teardown(tmem, bars);
 }
 
 // dw = the sum of `splits` partial sums of n elements each, in order.
@@ -385,10 +415,10 @@ constexpr int64_t MAX_SPLITS = 16;
 constexpr int64_t SPLIT_MIN_ROWS = 256;      // a piece of fewer rows does not pay for its partial sum
 constexpr int SM_COUNT = 152;                // what the workspace is sized for: the split must not need a device
 
-// Pieces of the contraction: as many as fill the SMs with jobs.
+// Pieces of the contraction: as many as fill the pairs of SMs with jobs.
 int64_t wgrad_splits(int64_t R, int64_t N, int64_t K, int64_t E) {
-    const int64_t jobs = E * ((N + BM - 1) / BM) * ((K + BN - 1) / BN);
-    int64_t s = SM_COUNT / jobs;
+    const int64_t jobs = E * ((N + TILE - 1) / TILE) * ((K + TILE - 1) / TILE);
+    int64_t s = SM_COUNT / 2 / jobs;
     const int64_t most = R / E / SPLIT_MIN_ROWS;
     if (s > most) s = most;
     if (s > MAX_SPLITS) s = MAX_SPLITS;
@@ -481,7 +511,8 @@ int situ_linear_wgrad(const void* dz, const void* a, const int64_t* expert_offse
     }
     const int64_t splits = wgrad_splits(R, N, K, E);
     const bool fp32 = splits > 1 || dw_type == SITU_FP32;
-    const int MT = (int)((N + BM - 1) / BM), NT = (int)((K + BN - 1) / BN);
+    const int MT = (int)((N + TILE - 1) / TILE), NT = (int)((K + TILE - 1) / TILE);
+    if (E * splits * MT * NT > INT32_MAX / 2) return SITU_GLU_INVALID_ARG;   // the kernel counts jobs in 32 bits
     CUtensorMap map_dz, map_a, map_dw;
     if (!make_map(&map_dz, dz, (uint64_t)R, (uint64_t)N, BK) || !make_map(&map_a, a, (uint64_t)R, (uint64_t)K, BK))
         return cuda_fail(cudaErrorInvalidValue);
@@ -491,15 +522,11 @@ int situ_linear_wgrad(const void* dz, const void* a, const int64_t* expert_offse
     const uint32_t box[3] = {(uint32_t)(128 / sz), 32, 1};
     if (!make_map_any(&map_dw, splits > 1 ? workspace : dw, fp32, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
         return cuda_fail(cudaErrorInvalidValue);
-    auto kernel = fp32 ? wgrad_kernel<true> : wgrad_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) return cuda_fail(e);
     int sms = 0;
     if ((st = sm_count(&sms)) != SITU_GLU_OK) return st;
-    const int64_t jobs = E * splits * MT * NT;
-    kernel<<<(unsigned)(jobs < sms ? jobs : sms), NUM_THREADS, SMEM_BYTES, stream>>>(
-        map_dz, map_a, map_dw, expert_offsets, status, (int)E, R, N, K, MT, NT, (int)splits);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+    cudaError_t e = launch_pairs(fp32 ? wgrad_kernel<true> : wgrad_kernel<false>, E * splits * MT * NT, NUM_THREADS, SMEM_BYTES,
+                                 stream, map_dz, map_a, map_dw, expert_offsets, status, (int)E, R, N, K, MT, NT, (int)splits);
+    if (e != cudaSuccess) return cuda_fail(e);
     if (splits > 1) {
         const int64_t n = E * N * K, blocks = (n / 4 + 255) / 256;
         const unsigned grid = (unsigned)(blocks < sms * 8 ? blocks : sms * 8);

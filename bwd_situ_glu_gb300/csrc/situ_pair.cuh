@@ -33,8 +33,8 @@ struct alignas(8) PairBars {
     uint64_t empty[PSTAGES];
     uint64_t tfull[2];
     uint64_t tempty[2];
-    uint64_t tail_full;                      // weight gradient: this CTA's loads of an expert's last, ragged stage
-    uint64_t tail_ready;                     // leader's: both CTAs have zeroed the rows past the expert's end
+    uint64_t tail_full[PSTAGES];             // weight gradient: this CTA's loads of an expert's last, ragged stage
+    uint64_t tail_ready[PSTAGES];            // leader's: both CTAs have zeroed the rows past the expert's end in it
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
@@ -173,13 +173,13 @@ __device__ __forceinline__ uint32_t pair_setup(PairBars* bars, int epi_warps) {
         for (int s = 0; s < PSTAGES; ++s) {
             mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->tail_full[s], 1);
+            mbar_init(&bars->tail_ready[s], 2);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&bars->tfull[a], 1);
             mbar_init(&bars->tempty[a], (uint32_t)(2 * epi_warps));
         }
-        mbar_init(&bars->tail_full, 1);
-        mbar_init(&bars->tail_ready, 2);
         mbar_init(&bars->mma_done, 1);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

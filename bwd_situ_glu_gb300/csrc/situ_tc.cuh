@@ -255,17 +255,6 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
         : "memory");
 }
 
-// The same with both operands MN-major ("transpose A" is bit 15): the weight gradient contracts over
-// rows, along which neither operand is contiguous.
-constexpr uint32_t IDESC_ABMN = IDESC | (1u << 15) | (1u << 16);
-__device__ __forceinline__ void tc_mma_abmn(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(
-            d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(IDESC_ABMN), "r"(accumulate)
-        : "memory");
-}
-
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
