@@ -26,7 +26,7 @@ using namespace situ_linear;
 // Rows are cut into pieces of PIECE rows of one expert; a block takes a piece's 256 columns at a time
 // (8 per lane, its warps take rows in turn), adds its warps' sums in order and leaves them in
 // part[piece][column]; the second kernel adds an expert's pieces in order. No result depends on timing.
-constexpr int PIECE = 256;
+constexpr int PIECE = 128;
 constexpr int BIAS_WARPS = 8;
 constexpr int BIAS_COLS = 256;
 
@@ -150,14 +150,15 @@ __global__ void __launch_bounds__(BIAS_COLS)
 //
 // The tensor cores cut each step's fp32 sum towards zero, an error that grows with the steps (measured
 // against float64 at 2048 x 2048: 5e-7 of the norm after 512 rows, 4.4e-6 after 4096, 1.9e-5 after
-// 16384). dW feeds an fp32 optimizer, so an accumulator takes at most CHUNK_BLOCKS stages (512 rows)
-// and the epilogue's threads add the chunks in registers, rounded to nearest, while the tensor cores
+// 16384). dW feeds an fp32 optimizer, so an accumulator takes CHUNK_BLOCKS stages (512 rows; up to three more
+// where that finishes the job) and the epilogue's threads add the chunks in registers, rounded to nearest, while the tensor cores
 // fill the other accumulator. Where the tiles of dW cannot fill the SMs, the rows are cut into `splits` pieces
 // whose sums (fp32, in the workspace) a second kernel adds in order.
-constexpr int CHUNK_BLOCKS = 8;
+constexpr int CHUNK_BLOCKS = 8, CHUNK_MORE = 3;
 constexpr int EPW = 2;
 constexpr int NUM_EPI_WARPS = 4 * EPW;
-constexpr int NUM_THREADS = 64 + NUM_EPI_WARPS * 32;
+constexpr int TAIL_WARP = 2 + NUM_EPI_WARPS;
+constexpr int NUM_THREADS = (3 + NUM_EPI_WARPS) * 32;   // TMA, MMA, epilogue, tails
 constexpr int TILE = 256;
 constexpr int STAGE_TILE = 32 * 128;         // 32 rows x 128 bytes of dW
 constexpr int SBYTES = PA_BYTES + PB_BYTES;
@@ -175,6 +176,14 @@ struct WJob {
     int mt, nt, plane;
     int row0, rows;                          // rows to contract over
 };
+
+// A job of kbs stages: whether its chunk ends with stage kb, in_chunk stages after the chunk's first, and its chunks.
+__device__ __forceinline__ bool chunk_ends_at(int kb, int in_chunk, int kbs) {
+    return kb + 1 == kbs || (in_chunk + 1 >= CHUNK_BLOCKS && kbs - kb - 1 > CHUNK_MORE);
+}
+__device__ __forceinline__ int chunk_count(int kbs) {
+    return kbs <= CHUNK_BLOCKS + CHUNK_MORE ? (kbs > 0) : 1 + (kbs - CHUNK_MORE - 1) / CHUNK_BLOCKS;
+}
 
 // Job j: experts, then pieces of their rows, then tiles of dW. 32-bit: the host bounds their number.
 __device__ __forceinline__ WJob wgrad_job(int j, const WPlan& plan, int E, int MT, int NT, int splits) {
@@ -266,50 +275,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int s = 0; s < STAGES_W; ++s)
             if (tail_used >> s & 1) mbar_drain(&bars->tail_full[s], (tail_next >> s & 1) ^ 1);
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer (leader); zeroing of ragged tails (both CTAs)
+        // ------------------------------------------------ MMA issuer (leader; the warp converged, one lane issues)
         const bool elected = elect_one();
         int stage = 0, done = 0;
-        uint32_t phase = 0, tails = 0;                           // bit s of tails: parity of stage s's ragged uses
+        uint32_t phase = 0, tails = 0;                           // bit s of tails: parity of stage s's next ragged use
         bool ok = true;
         const uint32_t idesc = pair_idesc(TILE, true, true);
         const uint32_t ring_addr = smem_addr(ring);
-        WJob next = wgrad_job(j0, plan, E, MT, NT, splits);
-        for (int j = j0; ok && j < jobs; j += jstep) {
-            const int rows = next.rows;
+        int rows_next = wgrad_job(j0, plan, E, MT, NT, splits).rows;
+        for (int j = j0; rank == 0 && ok && j < jobs; j += jstep) {
+            const int rows = rows_next;
             const int kbs = (rows + BK - 1) / BK;
-            if (j + jstep < jobs && (kbs == 0 || rank != 0)) next = wgrad_job(j + jstep, plan, E, MT, NT, splits);
-            if (rank != 0) {                                     // only the ragged stage of a job concerns this CTA
-                stage = (stage + kbs) % STAGES_W;
-                if ((rows & (UK - 1)) == 0) continue;
-            }
-            for (int kb = rank == 0 ? 0 : kbs - 1; kb < kbs; ++kb) {
-                const int valid = min(BK, rows - kb * BK), steps = (valid + UK - 1) / UK;
-                const int in_chunk = kb % CHUNK_BLOCKS, acc = done & 1;
-                const bool chunk_ends = in_chunk + 1 == CHUNK_BLOCKS || kb + 1 == kbs;
-                const int st = rank == 0 ? stage : (stage + STAGES_W - 1) % STAGES_W;
-                if (rank == 0) {
-                    if (in_chunk == 0) ok = pair_wait<true>(&bars->tempty[acc], (uint32_t)((done >> 1) & 1) ^ 1, &bars->abort, status);
-                    if (ok) ok = pair_wait(&bars->full[st], phase, &bars->abort, status);
-                }
-                if (ok && (valid & (UK - 1))) {                  // the job's last stage, its last step partial
-                    ok = pair_wait(&bars->tail_full[st], tails >> st & 1, &bars->abort, status);
-                    if (!ok) break;
-                    uint8_t* sa = ring + st * SBYTES;
-                    const int n16 = (steps * UK - valid) * 8;    // 16-byte pieces per box
-                    for (int i = lane; i < n16 * (SBYTES / PBOX_BYTES); i += 32) {
-                        const int box = i / n16;
-                        st_shared_v4(sa + box * PBOX_BYTES + valid * 128 + (i - box * n16) * 16, 0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars->tail_ready[st], 0));
-                    if (rank == 0) ok = pair_wait<true>(&bars->tail_ready[st], tails >> st & 1, &bars->abort, status);
-                    tails ^= 1u << st;
+            if (kbs == 0 && j + jstep < jobs) rows_next = wgrad_job(j + jstep, plan, E, MT, NT, splits).rows;
+            int in_chunk = 0;
+            for (int kb = 0; kb < kbs; ++kb) {
+                const int steps = (min(BK, rows - kb * BK) + UK - 1) / UK, acc = done & 1;
+                const bool chunk_ends = chunk_ends_at(kb, in_chunk, kbs);
+                if (in_chunk == 0) ok = pair_wait<true>(&bars->tempty[acc], (uint32_t)((done >> 1) & 1) ^ 1, &bars->abort, status);
+                if (ok) ok = pair_wait(&bars->full[stage], phase, &bars->abort, status);
+                if (ok && kb + 1 == kbs && (rows & (UK - 1))) {
+                    ok = pair_wait<true>(&bars->tail_ready[stage], tails >> stage & 1, &bars->abort, status);
+                    tails ^= 1u << stage;
                 }
                 if (!ok) break;
-                if (rank != 0) break;
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * 256), sa = ring_addr + (uint32_t)(st * SBYTES);
+                const uint32_t d = tmem + (uint32_t)(acc * 256), sa = ring_addr + (uint32_t)(stage * SBYTES);
                 const uint64_t ad = smem_desc_mn(sa), bd = smem_desc_mn(sa + PA_BYTES);
                 if (elected) {
 #pragma unroll
@@ -317,16 +307,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         if (kk < steps)
                             pair_mma(d, ad + (uint64_t)(kk * 128), bd + (uint64_t)(kk * 128), idesc,
                                      kk > 0 ? 1u : (uint32_t)in_chunk);
-                    pair_commit(&bars->empty[st]);
+                    pair_commit(&bars->empty[stage]);
                     if (chunk_ends) pair_commit(&bars->tfull[acc]);
                 }
                 done += chunk_ends;
+                in_chunk = chunk_ends ? 0 : in_chunk + 1;
                 if (++stage == STAGES_W) { stage = 0; phase ^= 1; }
-                if (kb == 0 && j + jstep < jobs) next = wgrad_job(j + jstep, plan, E, MT, NT, splits);   // while these run
+                if (kb == 0 && j + jstep < jobs) rows_next = wgrad_job(j + jstep, plan, E, MT, NT, splits).rows;   // while these run
             }
         }
         __syncwarp();
         if (rank == 0 && elected) pair_commit(&bars->mma_done);
+    } else if (warp == TAIL_WARP) {
+        // ------------------------------------------------ ragged tails (both CTAs): zeroed as soon as they land, while the
+        // stages before them are still being worked off (in the MMA warp this cost 1.1 us of every job)
+        int stage = 0;
+        uint32_t tails = 0;
+        bool ok = true;
+        for (int j = j0; ok && j < jobs; j += jstep) {
+            const int rows = wgrad_job(j, plan, E, MT, NT, splits).rows;
+            const int kbs = (rows + BK - 1) / BK;
+            const int st = (stage + kbs + STAGES_W - 1) % STAGES_W;          // the job's last stage
+            stage = (stage + kbs) % STAGES_W;
+            if ((rows & (UK - 1)) == 0) continue;
+            ok = pair_wait(&bars->tail_full[st], tails >> st & 1, &bars->abort, status);
+            if (!ok) break;
+            tails ^= 1u << st;
+            const int valid = rows - (kbs - 1) * BK;
+            const int n16 = (UK - (valid & (UK - 1))) * 8;                   // 16-byte pieces per box, to the step's end
+            uint8_t* sa = ring + st * SBYTES;
+            for (int i = lane; i < n16 * (SBYTES / PBOX_BYTES); i += 32) {
+                const int box = i / n16;
+                st_shared_v4(sa + box * PBOX_BYTES + valid * 128 + (i - box * n16) * 16, 0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars->tail_ready[st], 0));
+        }
     } else {
         // ------------------------------------------------ epilogue (both CTAs): a lane holds one row of dW
         const int quad = warp & 3;
@@ -339,7 +356,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int done = 0;
         for (int j = j0; j < jobs; j += jstep) {
             const WJob w = wgrad_job(j, plan, E, MT, NT, splits);
-            const int chunks = (w.rows + CHUNK_BLOCKS * BK - 1) / (CHUNK_BLOCKS * BK);
+            const int chunks = chunk_count((w.rows + BK - 1) / BK);
             bool ok = true;
             float sum[COLS];
 #pragma unroll

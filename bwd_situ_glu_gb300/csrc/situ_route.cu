@@ -6,14 +6,14 @@
 // Both are bound by HBM: the forward reads T·E scores once, the backward writes T·E once; at
 // T = 65537, E = 896 in fp32 that is 235 MB, 35 us at the measured copy rate, for each.
 //
-// Forward, one warp per token: lane i holds the scores i·W .. of each 32·W-wide chunk in registers
-// as order-preserving integers. A full sort or K rounds of a warp-wide maximum (K·(reduction +
-// rescan of a lane's 28 scores) ≈ 1100 instructions at E = 896, K = 16) would cost more issue slots
-// than the 35 us hold. Instead the K-th largest of the 32 lane maxima is a lower bound of the K-th
-// largest score, so only scores at or above it can be chosen; on random scores about 20 of 896 are
-// left, they fit one per lane, and one 32-wide bitonic sort of (score, index) finishes. Where more
-// than 32 are left (many equal scores, a sorted row), K rounds of a warp-wide maximum run instead:
-// the same result.
+// Forward, one warp per token: lane i holds the scores i·W .. of each 32·W-wide chunk in registers. The 35 us hold
+// some 600 instructions a token, and a full sort, or K rounds of a warp-wide maximum (K·(reduction + rescan of a
+// lane's 28 scores) ≈ 1100 at E = 896, K = 16), take more. Instead: the K-th largest of the 32 lane maxima is a
+// lower bound of the K-th largest score, so only scores at or above it can be chosen; on random scores about 20
+// of 896 are left, they fit one per lane, and one 32-wide bitonic sort of (score, index) finishes. The row
+// also goes to shared memory, from where a lane picks its candidates by a bit mask. Where more than 32 are left
+// (many equal scores, a sorted row), or a score is NaN, K rounds of a warp-wide maximum run instead: the
+// same result.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -71,29 +71,35 @@ template <bool BF16, int W, int C>
 __global__ void __launch_bounds__(WARPS * 32)
     route_topk_kernel(const void* __restrict__ logits, float* __restrict__ p, int32_t* __restrict__ ids, int64_t T,
                       int E, int K) {
+    constexpr int CHUNK = 32 * W;             // scores per chunk
     __shared__ uint32_t s_key[WARPS][32], s_idx[WARPS][32];
+    __shared__ float s_row[WARPS][C * CHUNK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * WARPS + warp;
     if (t >= T) return;
 
-    uint32_t key[C][W], top = 0;
-    float raw[C][W];
+    float v[C][W];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int e = (c * 32 + lane) * W;
-        if (e < E) load_scores<BF16, W>(logits, t * E + e, raw[c]);   // W divides E: whole vectors
+        const int e = c * CHUNK + lane * W;
+        if (e < E) {
+            load_scores<BF16, W>(logits, t * E + e, v[c]);      // W divides E: whole vectors
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[c][i] = -INFINITY;
+        }
     }
+    float top = -INFINITY;                    // the lane's maximum; NaN if it has one
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int e = (c * 32 + lane) * W;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            key[c][i] = e < E ? score_key(raw[c][i]) : 0u;
-            top = max(top, key[c][i]);
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(v[c][i]));
+            s_row[warp][c * CHUNK + lane * W + i] = v[c][i];
         }
     }
     // the K-th largest lane maximum (bitonic sort, descending over the lanes)
-    uint32_t srt = top;
+    uint32_t srt = score_key(top);
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
@@ -103,36 +109,37 @@ __global__ void __launch_bounds__(WARPS * 32)
             srt = keep_max ? max(srt, other) : min(srt, other);
         }
     }
-    const uint32_t bound = max(__shfl_sync(FULL, srt, K - 1), KEY_MINUS_INF + 1u);
+    const bool nan = __shfl_sync(FULL, srt, 0) == FULL;
+    // every score above -inf is at or above the lowest finite one
+    const float bound = fmaxf(key_score(__shfl_sync(FULL, srt, K - 1)), -3.402823466e38f);
 
-    int n = 0;
+    uint32_t mask = 0;                        // bit c·W + i: v[c][i] is a candidate
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < W; ++i) n += key[c][i] >= bound;
-    const int total = (int)__reduce_add_sync(FULL, (unsigned)n);
+        for (int i = 0; i < W; ++i) mask |= v[c][i] >= bound ? 1u << (c * W + i) : 0u;
+    const int n = __popc(mask);
+    int at = n;                               // inclusive prefix of n over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(FULL, at, o);
+        if (lane >= o) at += u;
+    }
+    const int total = __shfl_sync(FULL, at, 31);
 
     uint32_t my_key = 0, my_idx = FULL;       // lane k's result: the k-th largest
-    if (total <= 32) {
-        int at = n;                           // exclusive prefix of n over the lanes
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(FULL, at, o);
-            if (lane >= o) at += v;
-        }
+    if (total <= 32 && !nan) {
         at -= n;
         s_key[warp][lane] = 0;
         s_idx[warp][lane] = FULL;
         __syncwarp();
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                if (key[c][i] >= bound) {
-                    s_key[warp][at] = key[c][i];
-                    s_idx[warp][at] = (uint32_t)((c * 32 + lane) * W + i);
-                    ++at;
-                }
+        for (; mask; mask &= mask - 1) {
+            const int b = __ffs(mask) - 1;
+            const int idx = b / W * CHUNK + lane * W + b % W;
+            s_key[warp][at] = score_key(s_row[warp][idx]);      // this lane's own store
+            s_idx[warp][at] = (uint32_t)idx;
+            ++at;
+        }
         __syncwarp();
         my_key = s_key[warp][lane];
         my_idx = s_idx[warp][lane];
@@ -150,37 +157,32 @@ __global__ void __launch_bounds__(WARPS * 32)
             }
         }
     } else {
+        uint32_t taken = 0;                   // bit c·W + i: v[c][i] has been chosen
         for (int k = 0; k < K; ++k) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int i = 0; i < W; ++i) best = max(best, key[c][i]);
-            best = __reduce_max_sync(FULL, best);
-            if (best < bound) break;          // nothing above -inf is left
-            uint32_t idx = FULL;
-#pragma unroll
-            for (int c = C - 1; c >= 0; --c)
-#pragma unroll
-                for (int i = W - 1; i >= 0; --i)
-                    if (key[c][i] == best) idx = (uint32_t)((c * 32 + lane) * W + i);
-            idx = __reduce_min_sync(FULL, idx);
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    if ((uint32_t)((c * 32 + lane) * W + i) == idx) key[c][i] = 0;
+            uint32_t best = 0, idx = FULL;
+            for (int b = 0; b < C * W; ++b) { // from shared memory (this lane's own stores), so that no registers wait here
+                const int at_b = b / W * CHUNK + lane * W + b % W;
+                const uint32_t key = taken >> b & 1u ? 0u : score_key(s_row[warp][at_b]);
+                if (key > best) {
+                    best = key;
+                    idx = (uint32_t)at_b;
+                }
+            }
+            const uint32_t most = __reduce_max_sync(FULL, best);
+            if (most <= KEY_MINUS_INF) break; // nothing above -inf is left
+            const uint32_t first = __reduce_min_sync(FULL, best == most ? idx : FULL);
+            if (idx == first) taken |= 1u << (idx / CHUNK * W + idx % W);
             if (lane == k) {
-                my_key = best;
-                my_idx = idx;
+                my_key = most;
+                my_idx = first;
             }
         }
     }
 
     const bool live = lane < K && my_key > KEY_MINUS_INF;
-    const float v = key_score(my_key);
-    const float m = __shfl_sync(FULL, v, 0);  // unused where lane 0 is not live
-    const float ex = live ? expf(v - m) : 0.0f;
+    const float mine = key_score(my_key);
+    const float m = __shfl_sync(FULL, mine, 0);  // unused where lane 0 is not live
+    const float ex = live ? expf(mine - m) : 0.0f;
     const float sum = warp_sum(ex);
     if (lane < K) {
         p[t * K + lane] = live ? ex / sum : 0.0f;
