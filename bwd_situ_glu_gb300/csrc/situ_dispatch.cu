@@ -30,14 +30,26 @@ constexpr uint32_t FULL = 0xffffffffu;
 
 constexpr int PLAN_WARPS = 32;
 constexpr int PLAN_THREADS = PLAN_WARPS * 32;
-constexpr int64_t PLAN_ONE = 8192;           // ids that one block sorts alone
-constexpr int64_t PLAN_CHUNK = 4096;         // ids per block above that, until there are PLAN_BLOCKS
+constexpr int64_t PLAN_ONE = 4096;           // ids that one block sorts alone
+constexpr int64_t PLAN_CHUNK = 2048;         // ids per block above that, until there are PLAN_BLOCKS (262144 ids:
+                                             // 17 us; 4096 19 us, 8192 25 us)
 constexpr int64_t PLAN_BLOCKS = 152;         // one block per SM: the counts take 132 KB of its shared memory
 
 int64_t plan_blocks(int64_t n) {
     if (n <= PLAN_ONE) return 1;
     const int64_t b = (n + PLAN_CHUNK - 1) / PLAN_CHUNK;
     return b < PLAN_BLOCKS ? b : PLAN_BLOCKS;
+}
+
+// The lanes whose id equals this lane's, from one ballot per bit: some 30 instructions whatever the ids are
+// (__match_any_sync takes longer the more distinct ids there are: 262144 ids of 896 experts 31 us instead of 15).
+__device__ __forceinline__ uint32_t peers_of(uint32_t id, int bits) {
+    uint32_t peers = FULL;
+    for (int b = 0; b < bits; ++b) {
+        const uint32_t set = __ballot_sync(FULL, id >> b & 1u);
+        peers &= id >> b & 1u ? set : ~set;
+    }
+    return peers;
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS)
@@ -54,26 +66,27 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     for (int e = threadIdx.x; e < E; e += blockDim.x) counts[(int64_t)blockIdx.x * E + e] = hist[e];
 }
 
-// counts: [gridDim.x][E] of the first launch, or NULL with one block.
+// counts: [gridDim.x][E] of the first launch, or NULL with one block. `used`: warps that sort (all of them, or
+// fewer for few ids); bits: of an expert's number, E (no expert) included.
 __global__ void __launch_bounds__(PLAN_THREADS)
     plan_rows_kernel(const int32_t* __restrict__ ids, const float* __restrict__ p, const int* __restrict__ counts,
                      int64_t* __restrict__ offsets, int32_t* __restrict__ row_of, int32_t* __restrict__ src,
-                     float* __restrict__ p_rows, int64_t n, int E, int64_t chunk) {
-    extern __shared__ int cnt[];                 // [warps][E]: counts, then each warp's next row of each expert
+                     float* __restrict__ p_rows, int64_t n, int E, int64_t chunk, int used, int bits) {
+    extern __shared__ int cnt[];                 // [used][E]: counts, then each warp's next row of each expert
     __shared__ int s_warp[PLAN_WARPS];
     __shared__ int s_total;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int i = threadIdx.x; i < warps * E; i += blockDim.x) cnt[i] = 0;
+    for (int i = threadIdx.x; i < used * E; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
     // this warp's piece, whole steps of 32 ids
     const int64_t cb = blockIdx.x * chunk, ce = min(n, cb + chunk);
-    const int64_t piece = ((chunk + warps - 1) / warps + 31) / 32 * 32;
-    const int64_t b = min(ce, cb + warp * piece), en = min(ce, b + piece);
+    const int64_t piece = ((chunk + used - 1) / used + 31) / 32 * 32;
+    const int64_t b = warp < used ? min(ce, cb + warp * piece) : ce, en = min(ce, b + piece);
     int* mine = cnt + warp * E;
     for (int64_t i = b; i < en; i += 32) {
-        const int id = i + lane < en ? ids[i + lane] : -1;
-        const uint32_t peers = __match_any_sync(FULL, id);
-        if ((uint32_t)id < (uint32_t)E && lane == __ffs(peers) - 1) mine[id] += __popc(peers);
+        const uint32_t id = i + lane < en ? min((uint32_t)ids[i + lane], (uint32_t)E) : (uint32_t)E;
+        const uint32_t peers = peers_of(id, bits);
+        if (id < (uint32_t)E && lane == __ffs(peers) - 1) mine[id] += __popc(peers);
         __syncwarp();
     }
     __syncthreads();
@@ -82,7 +95,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     const int e = threadIdx.x;
     if (e < E) {
         int here = 0;
-        for (int w = 0; w < warps; ++w) here += cnt[w * E + e];
+        for (int w = 0; w < used; ++w) here += cnt[w * E + e];
         if (counts) {
             const int nb = (int)gridDim.x;
 #pragma unroll 8
@@ -121,7 +134,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
             offsets[e + 1] = incl;
         }
         int row = incl - all + before;
-        for (int w = 0; w < warps; ++w) {
+        for (int w = 0; w < used; ++w) {
             const int c = cnt[w * E + e];
             cnt[w * E + e] = row;
             row += c;
@@ -130,9 +143,9 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     __syncthreads();
     for (int64_t i = b; i < en; i += 32) {
         const bool in = i + lane < en;
-        const int id = in ? ids[i + lane] : -1;
-        const uint32_t peers = __match_any_sync(FULL, id);
-        const bool live = (uint32_t)id < (uint32_t)E;
+        const uint32_t id = in ? min((uint32_t)ids[i + lane], (uint32_t)E) : (uint32_t)E;
+        const uint32_t peers = peers_of(id, bits);
+        const bool live = id < (uint32_t)E;
         int row = -1;
         if (live) row = mine[id] + __popc(peers & ((1u << lane) - 1u));
         __syncwarp();
@@ -344,7 +357,7 @@ __global__ void __launch_bounds__(COPY_WARPS * 32)
     out.store(y, t * D + c * W);
 }
 
-constexpr int BWD_MAX_WARPS = 8;
+constexpr int BWD_MAX_WARPS = 4;              // 128 threads: 430 us at 196624 x 3584 (0.96 of the copy rate); 256: 468, 512: 564
 
 // One block takes a token: every thread holds vectors of dy and walks the token's rows, KB at a time
 // (so dy is read K/KB times, all but the first from L1), writing weight·dy and adding dy·o; the KB
@@ -483,14 +496,14 @@ int situ_dispatch_plan(const int32_t* ids, const float* p, int64_t* expert_offse
     const int64_t blocks = plan_blocks(n);
     const int64_t chunk = blocks > 1 ? (n + blocks - 1) / blocks : n;
     // few ids need few warps; expert e's prefix is thread e's, so at least E threads
-    int64_t threads = PLAN_THREADS;
-    if (blocks == 1) {
-        threads = ((n < 512 ? n : 512) + 31) / 32 * 32;
-        const int64_t te = (E + 31) / 32 * 32;
-        threads = threads < te ? te : threads;
-        if (n > 2048) threads = PLAN_THREADS;
+    int64_t threads = PLAN_THREADS, used = PLAN_WARPS;
+    if (chunk < PLAN_THREADS) {
+        used = chunk > 32 ? (chunk + 31) / 32 : 1;
+        threads = (E > used * 32 ? E + 31 : used * 32) / 32 * 32;
     }
-    const size_t smem = (size_t)(threads / 32) * E * 4;
+    int bits = 1;
+    while ((E >> bits) != 0) ++bits;
+    const size_t smem = (size_t)used * E * 4;
     cudaError_t ce = cudaFuncSetAttribute((const void*)plan_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           PLAN_WARPS * SITU_MAX_EXPERTS * 4);
     if (ce != cudaSuccess) return cuda_fail(ce);
@@ -500,7 +513,7 @@ int situ_dispatch_plan(const int32_t* ids, const float* p, int64_t* expert_offse
         if (st != SITU_GLU_OK) return st;
     }
     plan_rows_kernel<<<(unsigned)blocks, (unsigned)threads, smem, stream>>>(
-        ids, p, blocks > 1 ? (const int*)workspace : nullptr, expert_offsets, row_of, src, p_rows, n, (int)E, chunk);
+        ids, p, blocks > 1 ? (const int*)workspace : nullptr, expert_offsets, row_of, src, p_rows, n, (int)E, chunk, (int)used, bits);
     return launched();
 }
 
@@ -589,7 +602,7 @@ int situ_combine_bwd(const void* dy, const void* o, int type, const int32_t* row
     if ((st = sm_count(&sms)) != SITU_GLU_OK) return st;
     const bool vec = aligned(dy, 16) && aligned(o, 16) && aligned(dout_rows, 16) && D * sz % 16 == 0;
     const int W = vec ? (int)(16 / sz) : 1;
-    // threads: the row's vectors spread evenly over the fewest passes of at most 256 threads
+    // threads: the row's vectors spread evenly over the fewest passes of at most 128 threads
     const int64_t nv = D / W, passes = (nv + BWD_MAX_WARPS * 32 - 1) / (BWD_MAX_WARPS * 32);
     const int threads = (int)(((nv + passes - 1) / passes + 31) / 32 * 32);
     const int64_t most = (int64_t)sms * 64;

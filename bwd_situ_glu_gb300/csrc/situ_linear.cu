@@ -451,7 +451,7 @@ __device__ __forceinline__ void few_job(FewShared& sh, const uint16_t* a, const 
 }
 
 template <int ACT>
-__global__ void __launch_bounds__(FEW_WARPS * 32)
+__global__ void __launch_bounds__(FEW_WARPS * 32, 3)
     linear_few_kernel(const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, const int64_t* __restrict__ offsets,
                       const float* __restrict__ bias, const uint16_t* __restrict__ residual, void* __restrict__ out,
                       int out_fp32, uint16_t* __restrict__ pre, int E, int64_t R, int64_t N, int64_t K) {
