@@ -509,9 +509,11 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
 
 // ---------------------------------------------------------------- host side
 
-// Rows per expert up to which linear_few_kernel takes the forward (see there).
-constexpr int64_t FEW_MAX_MEAN_ROWS = 8;
-constexpr int64_t FEW_MAX_DENSE_ROWS = 64;
+// Up to how many rows linear_few_kernel takes the forward: on average two an expert, or 64 in all. 112 experts,
+// 3584 x 3072 (few / tensor-core kernel): 128 rows 244 / 249 us, 224 rows 327 / 333, 448 rows 369 / 361, 896 rows
+// 415 / 378; one weight: 1 row 7.0 / 14.6 us, 32 rows 11.5 / 14.7, 64 rows 14.2 / 14.4, 128 rows 24.7 / 14.6.
+constexpr int64_t FEW_MAX_MEAN_ROWS = 2;
+constexpr int64_t FEW_MAX_ROWS = 64;
 
 // Most rows per job. A job of n rows takes a 64-deep block in the larger of 2n cycles (tensor cores) and the time
 // its (256 + n)·64 bytes per SM need at ~50 bytes a cycle (measured), and jobs run in rounds over the pairs of
@@ -549,7 +551,10 @@ int launch_tc(const void* a, const void* w, const int64_t* offsets, int64_t E, c
     CUtensorMap map_w;
     RowMaps map_r;
     for (int i = 0; i < 4; ++i)
-        if (!make_map(&map_r.m[i], a, (uint64_t)R, (uint64_t)KC, 128u >> i)) return cuda_fail(cudaErrorInvalidValue);
+        // 128-byte promotion: rows off the 128-byte lines (K = 1000) bring fewer of their neighbours' sectors than with
+        // 256 (4099 x 3584 x 1000: 35.0 -> 32.5 us), the others do not care
+        if (!make_map(&map_r.m[i], a, (uint64_t)R, (uint64_t)KC, 128u >> i, BK, true, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
+            return cuda_fail(cudaErrorInvalidValue);
     // [E, N, K] as stored; forward: contraction K innermost, dgrad: output columns K innermost
     const uint64_t inner = (uint64_t)(W_MN ? NCOL : KC), rows = (uint64_t)(W_MN ? KC : NCOL);
     const uint64_t dims[3] = {inner, rows, (uint64_t)E}, strides[2] = {inner * 2, inner * rows * 2};
@@ -590,7 +595,7 @@ int launch_few(const void* a, const void* w, const int64_t* offsets, int64_t E, 
 template <int ACT>
 int launch_fwd(const void* a, const void* w, const int64_t* offsets, int64_t E, const float* bias, const void* residual,
                void* out, bool out_fp32, void* pre, int* status, int64_t R, int64_t N, int64_t K, cudaStream_t stream) {
-    const bool few = E == 1 ? R <= FEW_MAX_DENSE_ROWS : R <= E * FEW_MAX_MEAN_ROWS;
+    const bool few = R <= FEW_MAX_ROWS || R <= E * FEW_MAX_MEAN_ROWS;
     return few ? launch_few<ACT>(a, w, offsets, E, bias, residual, out, out_fp32, pre, R, N, K, stream)
                : launch_tc<false, ACT>(a, w, offsets, E, bias, residual, out, out_fp32, pre, status, R, N, K, stream);
 }
