@@ -21,6 +21,13 @@ import torch
 import bwd_situ_glu_gb300 as _sg
 from bwd_situ_glu_gb300 import _check, load as _lib
 
+# A decoding step's kernels take 3 to 5 us, an allocation and a launch through ctypes 5 us of host time; hence the
+# names bound here, the one expression per tensor in _need, and the raw stream handle (14.5 -> 9 us a call).
+_T, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64
+_CODE = {_BF16: 0, _F32: 1}  # SITU_BF16, SITU_FP32
+_empty = torch.empty
+_device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 MAX_EXPERTS, MAX_TOPK = 1024, 32  # SITU_MAX_EXPERTS, SITU_MAX_TOPK
 
@@ -47,28 +54,26 @@ def declare(lib):
 
 
 def _type(t, name):
-    if not isinstance(t, torch.Tensor):
+    """SITU_BF16 or SITU_FP32 of a tensor."""
+    if not isinstance(t, _T):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype == torch.bfloat16:
-        return 0
-    if t.dtype == torch.float32:
-        return 1
-    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return code
 
 
 def _two(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be two-dimensional, got {tuple(t.shape)}")
+    """The shape of a two-dimensional CUDA tensor."""
+    if not isinstance(t, _T):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a two-dimensional CUDA tensor, got {tuple(t.shape)} on {t.device}")
     return t.shape
 
 
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
-
-
-def _moved(stream, t):
-    """Whether the work runs elsewhere than on the current stream of the current device (see _elsewhere)."""
-    return stream is not None or t.device.index != torch._C._cuda_getDevice()
 
 
 def _elsewhere(stream, t, call):
@@ -82,24 +87,18 @@ def _elsewhere(stream, t, call):
             return call()
 
 
-def _current(t):
-    """Handle of the current stream of t's device. (The Stream object of torch.cuda.current_stream costs as
-    much as a decoding step's kernel: 5 us on the host.)"""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _need(t, dtype, shape, like, name):
-    """A contiguous tensor of this type and shape on the device of ``like``."""
-    if t.__class__ is not like.__class__ or t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+def _need(t, dtype, shape, dev, name):
+    """A contiguous tensor of this type and shape on this device."""
+    if t.__class__ is not _T or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
         _sg._need(t, dtype, shape, name)   # says what is wrong (a subclass of Tensor is fine)
-    if t.device != like.device:
-        raise ValueError("all tensors must be on the same device")
+        if t.device != dev:
+            raise ValueError("all tensors must be on the same device")
 
 
-def _out(t, shape, dtype, like, name):
+def _out(t, shape, dtype, dev, name):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _need(t, dtype, shape, like, name)
+        return _empty(shape, dtype=dtype, device=dev)
+    _need(t, dtype, shape, dev, name)
     return t
 
 
@@ -114,15 +113,14 @@ def situ_route_topk(logits, k, p=None, ids=None, stream=None):
     order, ties to the lower index. A score of -inf is never chosen (id -1, p 0). logits [T,E] bf16 or
     fp32, E <= 1024, k <= min(E, 32)."""
     ty = _type(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
-    T, E = logits.shape
-    _need(logits, logits.dtype, (T, E), logits, "logits")
-    if _moved(stream, logits):
+    T, E = _two(logits, "logits")
+    dev = logits.device
+    _need(logits, logits.dtype, (T, E), dev, "logits")
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, logits, lambda: situ_route_topk(logits, k, p, ids))
-    p = _out(p, (T, k), torch.float32, logits, "p")
-    ids = _out(ids, (T, k), torch.int32, logits, "ids")
-    _check(_lib().situ_route_topk(logits.data_ptr(), ty, p.data_ptr(), ids.data_ptr(), T, E, k, _current(logits)))
+    p = _out(p, (T, k), _F32, dev, "p")
+    ids = _out(ids, (T, k), _I32, dev, "ids")
+    _check(_lib().situ_route_topk(logits.data_ptr(), ty, p.data_ptr(), ids.data_ptr(), T, E, k, _raw_stream(dev.index)))
     return p, ids
 
 
@@ -130,22 +128,23 @@ def situ_route_topk_bwd(ids, p, dp, num_experts, dtype=None, row_of=None, dlogit
     """dlogits [T,num_experts] of ``dtype`` (default fp32): p_k(dp_k - sum_j p_j dp_j) at ids, 0 elsewhere.
     dp fp32 [T,k], or with ``row_of`` (int32 [T,k]) fp32 [R] in row order."""
     T, k = _two(ids, "ids")
-    _need(ids, torch.int32, (T, k), ids, "ids")
-    _need(p, torch.float32, (T, k), ids, "p")
+    dev = ids.device
+    _need(ids, _I32, (T, k), dev, "ids")
+    _need(p, _F32, (T, k), dev, "p")
     R = 0
     if row_of is None:
-        _need(dp, torch.float32, (T, k), ids, "dp")
+        _need(dp, _F32, (T, k), dev, "dp")
     else:
-        _need(row_of, torch.int32, (T, k), ids, "row_of")
+        _need(row_of, _I32, (T, k), dev, "row_of")
         R = dp.numel()
-        _need(dp, torch.float32, (R,), ids, "dp")
-    if _moved(stream, ids):
+        _need(dp, _F32, (R,), dev, "dp")
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, ids, lambda: situ_route_topk_bwd(ids, p, dp, num_experts, dtype, row_of, dlogits))
     if dlogits is not None:
         dtype = dlogits.dtype
-    dlogits = _out(dlogits, (T, num_experts), dtype or torch.float32, ids, "dlogits")
+    dlogits = _out(dlogits, (T, num_experts), dtype or _F32, dev, "dlogits")
     _check(_lib().situ_route_topk_bwd(ids.data_ptr(), p.data_ptr(), dp.data_ptr(), _ptr(row_of), R, dlogits.data_ptr(),
-                                      _type(dlogits, "dlogits"), T, num_experts, k, _current(ids)))
+                                      _type(dlogits, "dlogits"), T, num_experts, k, _raw_stream(dev.index)))
     return dlogits
 
 
@@ -156,21 +155,22 @@ def situ_dispatch_plan(ids, num_experts, p=None, stream=None):
     of the token-expert pairs, sorted by expert and, within one, by token and choice. An id outside
     [0, num_experts) has no row (row_of -1); src past the last row is -1, p_rows 0."""
     T, k = _two(ids, "ids")
-    _need(ids, torch.int32, (T, k), ids, "ids")
+    dev = ids.device
+    _need(ids, _I32, (T, k), dev, "ids")
     if p is not None:
-        _need(p, torch.float32, (T, k), ids, "p")
-    if _moved(stream, ids):
+        _need(p, _F32, (T, k), dev, "p")
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, ids, lambda: situ_dispatch_plan(ids, num_experts, p))
-    lib, dev, n = _lib(), ids.device, T * k
-    offsets = torch.empty(max(0, num_experts + 1), dtype=torch.int64, device=dev)
-    row_of = torch.empty((T, k), dtype=torch.int32, device=dev)
-    src = torch.empty(n, dtype=torch.int32, device=dev)
-    p_rows = None if p is None else torch.empty(n, dtype=torch.float32, device=dev)
+    lib, n = _lib(), T * k
+    offsets = _empty(max(0, num_experts + 1), dtype=_I64, device=dev)
+    row_of = _empty((T, k), dtype=_I32, device=dev)
+    src = _empty(n, dtype=_I32, device=dev)
+    p_rows = None if p is None else _empty(n, dtype=_F32, device=dev)
     nb = lib.situ_dispatch_plan_workspace(T, k, num_experts)
     ws = _scratch(nb, ids)
     # without tokens there is nothing to weigh: the pointers of empty tensors are null
     _check(lib.situ_dispatch_plan(ids.data_ptr(), _ptr(p), offsets.data_ptr(), row_of.data_ptr(), src.data_ptr(),
-                                  _ptr(p_rows), _ptr(ws), nb, T, k, num_experts, _current(ids)))
+                                  _ptr(p_rows), _ptr(ws), nb, T, k, num_experts, _raw_stream(dev.index)))
     return offsets, row_of, src, p_rows
 
 
@@ -179,17 +179,18 @@ def situ_dispatch(x, row_of, expert_offsets, weights=None, h=None, stream=None):
     token are zero. x [T,D] bf16 or fp32."""
     ty = _type(x, "x")
     (T, D), k = _two(x, "x"), _two(row_of, "row_of")[1]
-    _need(x, x.dtype, (T, D), x, "x")
-    _need(row_of, torch.int32, (T, k), x, "row_of")
+    dev = x.device
+    _need(x, x.dtype, (T, D), dev, "x")
+    _need(row_of, _I32, (T, k), dev, "row_of")
     E = expert_offsets.numel() - 1
-    _need(expert_offsets, torch.int64, (E + 1,), x, "expert_offsets")
+    _need(expert_offsets, _I64, (E + 1,), dev, "expert_offsets")
     if weights is not None:
-        _need(weights, torch.float32, (T, k), x, "weights")
-    if _moved(stream, x):
+        _need(weights, _F32, (T, k), dev, "weights")
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, x, lambda: situ_dispatch(x, row_of, expert_offsets, weights, h))
-    h = _out(h, (T * k, D), x.dtype, x, "h")
+    h = _out(h, (T * k, D), x.dtype, dev, "h")
     _check(_lib().situ_dispatch(x.data_ptr(), ty, row_of.data_ptr(), expert_offsets.data_ptr(), E, _ptr(weights),
-                                h.data_ptr(), T, k, T * k, D, _current(x)))
+                                h.data_ptr(), T, k, T * k, D, _raw_stream(dev.index)))
     return h
 
 
@@ -198,17 +199,18 @@ def situ_combine(o, row_of, weights=None, residual=None, y=None, stream=None):
     rounded once). o [R,D] bf16 or fp32; ``y`` may be ``residual`` itself."""
     ty = _type(o, "o")
     (R, D), (T, k) = _two(o, "o"), _two(row_of, "row_of")
-    _need(o, o.dtype, (R, D), o, "o")
-    _need(row_of, torch.int32, (T, k), o, "row_of")
+    dev = o.device
+    _need(o, o.dtype, (R, D), dev, "o")
+    _need(row_of, _I32, (T, k), dev, "row_of")
     if weights is not None:
-        _need(weights, torch.float32, (T, k), o, "weights")
+        _need(weights, _F32, (T, k), dev, "weights")
     if residual is not None:
-        _need(residual, o.dtype, (T, D), o, "residual")
-    if _moved(stream, o):
+        _need(residual, o.dtype, (T, D), dev, "residual")
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, o, lambda: situ_combine(o, row_of, weights, residual, y))
-    y = _out(y, (T, D), o.dtype, o, "y")
+    y = _out(y, (T, D), o.dtype, dev, "y")
     _check(_lib().situ_combine(o.data_ptr(), ty, row_of.data_ptr(), _ptr(weights), _ptr(residual), y.data_ptr(), T, k,
-                               R, D, _current(o)))
+                               R, D, _raw_stream(dev.index)))
     return y
 
 
@@ -217,19 +219,20 @@ def situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do=None, dweights=N
     zero), dweights[t,j] = <dy[t], o[row_of[t,j]]> (0 without a row)."""
     ty = _type(o, "o")
     (R, D), (T, k) = _two(o, "o"), _two(row_of, "row_of")
-    _need(o, o.dtype, (R, D), o, "o")
-    _need(dy, o.dtype, (T, D), o, "dy")
-    _need(row_of, torch.int32, (T, k), o, "row_of")
-    _need(weights, torch.float32, (T, k), o, "weights")
+    dev = o.device
+    _need(o, o.dtype, (R, D), dev, "o")
+    _need(dy, o.dtype, (T, D), dev, "dy")
+    _need(row_of, _I32, (T, k), dev, "row_of")
+    _need(weights, _F32, (T, k), dev, "weights")
     E = expert_offsets.numel() - 1
-    _need(expert_offsets, torch.int64, (E + 1,), o, "expert_offsets")
-    if _moved(stream, o):
+    _need(expert_offsets, _I64, (E + 1,), dev, "expert_offsets")
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, o, lambda: situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do, dweights))
-    do = _out(do, (R, D), o.dtype, o, "do")
-    dweights = _out(dweights, (T, k), torch.float32, o, "dweights")
+    do = _out(do, (R, D), o.dtype, dev, "do")
+    dweights = _out(dweights, (T, k), _F32, dev, "dweights")
     _check(_lib().situ_combine_bwd(dy.data_ptr(), o.data_ptr(), ty, row_of.data_ptr(), weights.data_ptr(),
                                    expert_offsets.data_ptr(), E, do.data_ptr(), dweights.data_ptr(), T, k, R, D,
-                                   _current(o)))
+                                   _raw_stream(dev.index)))
     return do, dweights
 
 
@@ -237,8 +240,7 @@ def situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do=None, dweights=N
 
 def _linear_shape(a, w, expert_offsets, a_name="a"):
     """(R, N, K, E, lead): w is [N,K] without expert_offsets, [E,N,K] with them; lead is () or (E,)."""
-    _type(a, a_name)
-    R = _two(a, a_name)[0]
+    R, dev = _two(a, a_name)[0], a.device
     if expert_offsets is None:
         if w.dim() != 2:
             raise ValueError("w must be [N, K] without expert_offsets")
@@ -249,8 +251,8 @@ def _linear_shape(a, w, expert_offsets, a_name="a"):
             raise ValueError("w must be [E, N, K] with expert_offsets")
         E, N, K = w.shape
         lead = (E,)
-        _need(expert_offsets, torch.int64, (E + 1,), a, "expert_offsets")
-    _need(w, torch.bfloat16, (*lead, N, K), a, "w")
+        _need(expert_offsets, _I64, (E + 1,), dev, "expert_offsets")
+    _need(w, _BF16, (*lead, N, K), dev, "w")
     return R, N, K, E, lead
 
 
@@ -270,23 +272,24 @@ def situ_linear(a, w, expert_offsets=None, bias=None, residual=None, act="none",
     situ_linear_bwd. N and K multiples of 8. ``status`` (int32 [1] on the device, zeroed by the caller)
     turns 1 if a pipeline wait timed out."""
     R, N, K, E, lead = _linear_shape(a, w, expert_offsets)
-    _need(a, torch.bfloat16, (R, K), a, "a")
+    dev = a.device
+    _need(a, _BF16, (R, K), dev, "a")
     if bias is not None:
-        _need(bias, torch.float32, (*lead, N), a, "bias")
+        _need(bias, _F32, (*lead, N), dev, "bias")
     if residual is not None:
-        _need(residual, torch.bfloat16, (R, N), a, "residual")
+        _need(residual, _BF16, (R, N), dev, "residual")
     if status is not None:
-        _need(status, torch.int32, (1,), a, "status")
+        _need(status, _I32, (1,), dev, "status")
     code = _act(act)
-    if _moved(stream, a):
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, a, lambda: situ_linear(a, w, expert_offsets, bias, residual, act, save_pre, out,
                                                          out_dtype, status))
     if out is not None:
         out_dtype = out.dtype
-    out = _out(out, (R, N), out_dtype or torch.bfloat16, a, "out")
-    pre = torch.empty((R, N), dtype=torch.bfloat16, device=a.device) if save_pre else None
+    out = _out(out, (R, N), out_dtype or _BF16, dev, "out")
+    pre = _empty((R, N), dtype=_BF16, device=a.device) if save_pre else None
     _check(_lib().situ_linear_fwd(a.data_ptr(), w.data_ptr(), _ptr(expert_offsets), E, _ptr(bias), _ptr(residual), code,
-                                  out.data_ptr(), _type(out, "out"), _ptr(pre), _ptr(status), R, N, K, _current(a)))
+                                  out.data_ptr(), _type(out, "out"), _ptr(pre), _ptr(status), R, N, K, _raw_stream(dev.index)))
     return (out, pre) if save_pre else out
 
 
@@ -298,39 +301,40 @@ def situ_linear_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, dw_dt
     of the unrounded dz). What is not asked for (bias, need_da, need_dw) is None. An expert without rows
     gets zeros in dw and dbias; da of rows of no expert is not written."""
     R, N, K, E, lead = _linear_shape(dout, w, expert_offsets, "dout")
-    _need(dout, torch.bfloat16, (R, N), dout, "dout")
+    dev = dout.device
+    _need(dout, _BF16, (R, N), dev, "dout")
     if need_dw:
-        _need(a, torch.bfloat16, (R, K), dout, "a")
+        _need(a, _BF16, (R, K), dev, "a")
     code = _act(act)
     if code:
         if pre is None:
             raise ValueError(f"act {act!r} needs the saved pre (situ_linear with save_pre=True)")
-        _need(pre, torch.bfloat16, (R, N), dout, "pre")
+        _need(pre, _BF16, (R, N), dev, "pre")
     else:
         pre = None
     if status is not None:
-        _need(status, torch.int32, (1,), dout, "status")
-    if _moved(stream, dout):
+        _need(status, _I32, (1,), dev, "status")
+    if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, dout, lambda: situ_linear_bwd(dout, a, w, expert_offsets, act, pre, dw_dtype, bias,
                                                                 need_da, need_dw, status))
-    lib, dev, s = _lib(), dout.device, _current(dout)
+    lib, s = _lib(), _raw_stream(dev.index)
     da = dw = dbias = None
     dz, off = dout, _ptr(expert_offsets)
     if code or bias:
         if code:
-            dz = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+            dz = _empty((R, N), dtype=_BF16, device=dev)
         nb, ws = 0, None
         if bias:
-            dbias = torch.empty((*lead, N), dtype=torch.float32, device=dev)
+            dbias = _empty((*lead, N), dtype=_F32, device=dev)
             nb = lib.situ_linear_act_bwd_workspace(R, N, E)
             ws = _scratch(nb, dout)
         _check(lib.situ_linear_act_bwd(dout.data_ptr(), _ptr(pre), code, off, E, dz.data_ptr() if code else 0,
                                        _ptr(dbias), _ptr(ws), nb, R, N, s))
     if need_da:
-        da = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
+        da = _empty((R, K), dtype=_BF16, device=dev)
         _check(lib.situ_linear_dgrad(dz.data_ptr(), w.data_ptr(), off, E, da.data_ptr(), _ptr(status), R, N, K, s))
     if need_dw:
-        dw = torch.empty((*lead, N, K), dtype=dw_dtype or torch.float32, device=dev)
+        dw = _empty((*lead, N, K), dtype=dw_dtype or _F32, device=dev)
         nb = lib.situ_linear_wgrad_workspace(R, N, K, E)
         ws = _scratch(nb, dout)
         _check(lib.situ_linear_wgrad(dz.data_ptr(), a.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"), _ptr(ws), nb,
@@ -401,7 +405,7 @@ def _autograd():
             a, w, expert_offsets, pre = ctx.saved_tensors
             need = ctx.needs_input_grad
             dout = dout.contiguous()
-            da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=torch.bfloat16,
+            da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=_BF16,
                                          bias=need[2], need_da=need[0], need_dw=need[1])
             return da, dw, db, dout if need[3] else None, None, None
 
