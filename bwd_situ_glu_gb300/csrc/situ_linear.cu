@@ -47,7 +47,7 @@ __host__ __device__ constexpr int ring_stages(int most) {
     const int s = PRING_BYTES / stage_bytes(most);
     return s < PSTAGES ? s : PSTAGES;
 }
-static_assert(ring_stages(MAX_CHUNK) == 6, "ring");
+static_assert(ring_stages(MAX_CHUNK) == 6 && ring_stages(192) == 7, "ring");
 
 struct Job {
     int e, nt;
@@ -305,39 +305,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     fetch_residual(c + EPW * CW);
                 }
                 tc_wait_ld();
-                float z[4][8];                               // [8-row group][column block 2: 0, 8, 16, 24][2 rows]
+                float2 z[4][4];                              // [8-row group][column block: 0, 8, 16, 24] two rows
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) z[g][i] = __uint_as_float(v[i >> 2][4 * g + (i & 3)]) + b[i >> 1];
+                    for (int i = 0; i < 4; ++i)
+                        z[g][i] = __fadd2_rn(make_float2(__uint_as_float(v[i >> 1][4 * g + 2 * (i & 1)]),
+                                                         __uint_as_float(v[i >> 1][4 * g + 2 * (i & 1) + 1])),
+                                             make_float2(b[i], b[i]));
+                if (pre) __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t at_g = patch_addr + patch_at(8 * g + (lane & 7), lane >> 3);
+                    uint32_t r[4];
+                    if (residual) ld_matrix_t(at_g, r);
+                    if (pre) {
+                        __syncwarp();
+                        st_matrix_t(at_g, pack_bf16x2(z[g][0].x, z[g][0].y), pack_bf16x2(z[g][1].x, z[g][1].y),
+                                    pack_bf16x2(z[g][2].x, z[g][2].y), pack_bf16x2(z[g][3].x, z[g][3].y));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        z[g][i] = act_pair<ACT>(z[g][i]);
+                        if (residual) z[g][i] = __fadd2_rn(z[g][i], make_float2(bf16_lo(r[i]), bf16_hi(r[i])));
+                    }
+                }
                 if (pre) {
                     __syncwarp();
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t r[4];
-                        if (residual) ld_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), r);
-                        __syncwarp();
-                        st_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), pack_bf16x2(z[g][0], z[g][1]),
-                                    pack_bf16x2(z[g][2], z[g][3]), pack_bf16x2(z[g][4], z[g][5]), pack_bf16x2(z[g][6], z[g][7]));
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            z[g][i] = act_value<ACT>(z[g][i]);
-                            if (residual) z[g][i] += i & 1 ? bf16_hi(r[i >> 1]) : bf16_lo(r[i >> 1]);
-                        }
-                    }
-                    __syncwarp();
                     patch_out(patch, pre, at, NCOL, left, ncols, lane);
-                } else {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t r[4];
-                        if (residual) ld_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), r);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            z[g][i] = act_value<ACT>(z[g][i]);
-                            if (residual) z[g][i] += i & 1 ? bf16_hi(r[i >> 1]) : bf16_lo(r[i >> 1]);
-                        }
-                    }
                 }
                 if (out_fp32) {                              // 8 lanes' columns of a row: 32 bytes
 #pragma unroll
@@ -345,14 +340,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int r = 8 * g + 2 * (lane & 3) + (i & 1), cc = (lane >> 2) + 8 * (i >> 1);
-                            if (r < left && cc < ncols) ((float*)out)[at + (int64_t)r * NCOL + cc] = z[g][i];
+                            if (r < left && cc < ncols)
+                                ((float*)out)[at + (int64_t)r * NCOL + cc] = i & 1 ? z[g][i >> 1].y : z[g][i >> 1].x;
                         }
                 } else {
                     __syncwarp();
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
-                        st_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), pack_bf16x2(z[g][0], z[g][1]),
-                                    pack_bf16x2(z[g][2], z[g][3]), pack_bf16x2(z[g][4], z[g][5]), pack_bf16x2(z[g][6], z[g][7]));
+                        st_matrix_t(patch_addr + patch_at(8 * g + (lane & 7), lane >> 3), pack_bf16x2(z[g][0].x, z[g][0].y),
+                                    pack_bf16x2(z[g][1].x, z[g][1].y), pack_bf16x2(z[g][2].x, z[g][2].y),
+                                    pack_bf16x2(z[g][3].x, z[g][3].y));
                     __syncwarp();
                     patch_out(patch, (uint16_t*)out, at, NCOL, left, ncols, lane);
                 }
@@ -517,8 +514,9 @@ constexpr int64_t FEW_MAX_ROWS = 64;
 
 // Most rows per job. A job of n rows takes a 64-deep block in the larger of 2n cycles (tensor cores) and the time
 // its (256 + n)·64 bytes per SM need at ~50 bytes a cycle (measured), and jobs run in rounds over the pairs of
-// SMs: 256 rows for large shapes, less where that would leave pairs without a job or a round mostly empty.
-// 4096 x 3584 x 3584 takes 256 rows (3 rounds), 256 x 3584 x 3584 takes 64 (56 jobs).
+// SMs: 256 rows for large shapes, less where that would leave pairs without a job or a round mostly empty. A ring
+// stage is sized for them: with weights streamed from HBM the loads in flight count (112 experts of ~292 rows: five
+// 32 KB stages 562 us, six 523).
 int64_t block_cycles(int64_t n) {
     const int64_t bytes = (256 + n) * 64 / 50;
     return 2 * n > bytes ? 2 * n : bytes;
@@ -537,11 +535,13 @@ int pick_chunk(int64_t R, int64_t E, int NT, int64_t KB, int pairs) {
         const int64_t each = KB * block_cycles(n) + 4 * n + 1500, tail = KB * block_cycles(last) + 4 * last + 1500;
         // many rounds even out over ragged experts; few do not
         const int64_t cost = rounds >= 16 ? (full * each + part * tail) / pairs : rounds * each + more * tail;
-        if (cost < best_cost) {
+        if (cost <= best_cost) {             // of equal chunks the tightest bound: smaller stages, more of them
             best_cost = cost;
             best = most;
         }
     }
+    // ragged experts: those with more rows than the average should not be cut for it (each chunk reads the weights again)
+    if (E > 1 && E * NT >= pairs) best = 4 * best < MAX_CHUNK ? 4 * best : MAX_CHUNK;
     return best;
 }
 

@@ -25,7 +25,7 @@ using namespace situ_tc;
 constexpr int PSTAGES = 8;                   // most stages of a ring (barriers); a kernel may use fewer, larger ones
 constexpr int PA_BYTES = 128 * BK * 2;       // this CTA's 128 rows of A (or columns, MN-major)
 constexpr int PB_BYTES = 128 * BK * 2;       // this CTA's half of 256 rows of B (or columns)
-constexpr int PRING_BYTES = 192 * 1024;
+constexpr int PRING_BYTES = 196 * 1024;     // 6 stages for 256 rows of B, 7 for 192, 8 for 128
 constexpr int PBOX_BYTES = 64 * BK * 2;      // an MN-major box: 64 columns x 64 deep
 
 struct alignas(8) PairBars {
