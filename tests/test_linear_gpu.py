@@ -100,6 +100,63 @@ def test_rows_of_no_expert_are_untouched(counts):
     check_fwd(counts, 264, 72, "silu", True, True, BF, False, tail=37)
 
 
+@pytest.mark.parametrize("R", [37, 400])
+def test_no_expert_has_rows(R):
+    """Rows, but every expert empty: nothing is written, the weights' gradients are zero."""
+    check_fwd([0, 0, 0], 264, 72, "none", True, False, BF, False, tail=R)
+    off = torch.zeros(4, dtype=torch.int64, device=DEV)
+    z = lambda *s: torch.ones(s, dtype=BF, device=DEV)  # noqa: E731
+    for dtype in (torch.float32, BF):
+        _, dw, db = sg.situ_linear_bwd(z(R, 264), z(R, 72), z(3, 264, 72), off, dw_dtype=dtype)
+        assert (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("R,E,owner", [(64, 100, 57), (150, 100, 99), (300, 20, 0), (700, 3, 1)])
+def test_one_expert_has_all_rows(R, E, owner):
+    """The choice of kernel and chunk goes by the average: the worst case against it is still right."""
+    counts = [0] * E
+    counts[owner] = R
+    check_fwd(counts, 72, 136, "silu", True, True, BF, True)
+    check_bwd(counts, 72, 136, "none", torch.float32)
+
+
+def test_more_experts_than_rows():
+    counts = ([0, 1, 0, 2, 0, 0, 3] * 147)[:1024]
+    check_fwd(counts, 40, 24, "none", True, False, BF, False)
+    check_bwd(counts, 40, 24, "none", torch.float32)
+
+
+def near_rows(got, want, tol):
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+def test_offsets_past_32_bits():
+    """out, the weights and the weight gradient each larger than 2^31 elements: places at both ends are right."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    new = lambda *s: torch.randn(*s, generator=g, device=DEV, dtype=BF)  # noqa: E731
+    R, N, K = 2_200_000, 1000, 8                        # 2.2e9 outputs and residuals
+    a, w, res = new(R, K), new(N, K), new(R, N)
+    out = sg.situ_linear(a, w, residual=res)
+    for rows in (slice(0, 50), slice(R - 50, R), slice(2 ** 31 // N - 25, 2 ** 31 // N + 25)):
+        z = a[rows].double() @ w.double().t()
+        near_rows(out[rows], z + res[rows].double(), steps_tol(K, a[rows].double().abs() @ w.double().abs().t()) + 1.01 * ref.BF16_HALF * (z + res[rows].double()).abs())
+    del a, w, res, out
+    E, N, K = 600, 1024, 3584                           # 2.2e9 weights
+    w = new(E, N, K)
+    for per in (1, 5):                                   # streamed, and tiled
+        off = (torch.arange(E + 1, device=DEV) * per)
+        a = new(E * per, K)
+        out = sg.situ_linear(a, w, off)
+        dz = new(E * per, N)
+        da, dw, _ = sg.situ_linear_bwd(dz, a, w, off, bias=False)
+        for e in (0, 1, 585, E - 1):
+            r = slice(e * per, (e + 1) * per)
+            W, A, Z = w[e].double(), a[r].double(), dz[r].double()
+            near_rows(out[r], A @ W.t(), steps_tol(K, A.abs() @ W.abs().t()) + 1.01 * ref.BF16_HALF * (A @ W.t()).abs())
+            near_rows(da[r], Z @ W, steps_tol(N, Z.abs() @ W.abs()) + 1.01 * ref.BF16_HALF * (Z @ W).abs())
+            near_rows(dw[e], Z.t() @ A, steps_tol(per, Z.abs().t() @ A.abs()) + 2 * ref.U24 * (Z.t() @ A).abs())
+
+
 def test_large_values_and_saturation():
     """Activations far from zero: gelu and silu go to 0 on the left and z on the right, nothing turns NaN."""
     K = N = 64

@@ -255,6 +255,28 @@ def test_combine_gradient_by_differences():
         assert abs(num - (np64(grad) * np64(v)).sum()) <= 20 * 8 * ref.U24 * mag / eps
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of rows: tokens at both ends are right."""
+    T, K, E, D = 38000, 16, 896, 3584                   # 2.18e9 elements
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ids = torch.topk(torch.rand(T, E, generator=g, device=DEV), K, dim=1).indices.to(torch.int32)
+    offsets, row_of, src, _ = sg.situ_dispatch_plan(ids, E)
+    assert torch.equal(src.sort().values, torch.arange(T * K, dtype=torch.int32, device=DEV))
+    x = torch.randn(T, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    w = torch.rand(T, K, generator=g, device=DEV)
+    h = sg.situ_dispatch(x, row_of, offsets)
+    for r in (slice(0, 40), slice(2 ** 31 // D - 20, 2 ** 31 // D + 20), slice(T * K - 40, T * K)):
+        assert torch.equal(h[r], x[(src[r] // K).long()])
+    y = sg.situ_combine(h, row_of, weights=w)
+    do, dw = sg.situ_combine_bwd(x, h, row_of, w, offsets)
+    for t in (0, 1, T // 2, T - 1):
+        rows, xt, wt = row_of[t].long(), x[t].double(), w[t].double()
+        near = lambda got, want, tol: ((got.double() - want).abs() <= tol).all()  # noqa: E731
+        assert near(y[t], xt * wt.sum(), (K + 2) * ref.U24 * (xt.abs() * wt.sum()) + HALF[torch.bfloat16] * (xt * wt.sum()).abs())
+        assert near(do[rows], wt[:, None] * xt, HALF[torch.bfloat16] * (wt[:, None] * xt).abs())
+        assert near(dw[t], (xt * xt).sum().expand(K), (D / 128 + 8 + 5 + 8 + 2) * ref.U24 * (xt * xt).sum())
+
+
 def test_rows_out_of_range_are_skipped():
     """row_of entries at or past R, and negative ones, are neither read nor written."""
     o = torch.ones(4, 8, device=DEV)
