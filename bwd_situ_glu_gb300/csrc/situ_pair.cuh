@@ -40,6 +40,7 @@ struct alignas(8) PairBars {
     int abort;
 };
 
+// One poll: the thread is suspended until the phase completes or about SUSPEND_NS have passed.
 constexpr uint32_t SUSPEND_NS = 20000;
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* b, uint32_t parity) {
     uint32_t ok;
@@ -50,18 +51,6 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* b, uint32_t parity) {
         : "r"(smem_addr(b)), "r"(parity), "r"(SUSPEND_NS)
         : "memory");
     return ok != 0;
-}
-
-// Without suspension, of a converged warp: has the phase completed?
-__device__ __forceinline__ bool pair_test_cluster(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_addr(b)), "r"(parity)
-        : "memory");
-    return __all_sync(0xffffffffu, ok != 0);
 }
 
 __device__ __forceinline__ bool try_wait_cta(uint64_t* b, uint32_t parity) {
@@ -81,7 +70,7 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Bounded wait of a converged warp (2 s, or WAIT_LIMIT polls): on a timeout sets the CTA's abort flag and the
+// Bounded wait of a converged warp (2 s by %globaltimer, or POLL_LIMIT polls): on a timeout sets the CTA's abort flag and the
 // caller's status word; returns false then, and once another role of the CTA has aborted, to all lanes alike.
 // CLUSTER: acquire at cluster scope, for barriers at which threads of the other CTA arrive.
 //
@@ -92,13 +81,14 @@ __device__ __forceinline__ bool elect_one() {
 // coordinates uniform over the warp: in a single-lane branch each MMA and load first moved six values to
 // uniform registers.
 constexpr uint32_t FREE_POLLS = 16;
+constexpr uint32_t POLL_LIMIT = 1u << 19;    // of at most 20 us: some ten seconds
 
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool pair_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
     for (uint32_t i = 0; i < FREE_POLLS; ++i)
         if (__all_sync(0xffffffffu, CLUSTER ? try_wait_cluster(b, parity) : try_wait_cta(b, parity))) return true;
     const uint64_t t0 = global_ns();
-    for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
+    for (uint32_t i = 0; i < POLL_LIMIT; ++i) {
         if (__all_sync(0xffffffffu, CLUSTER ? try_wait_cluster(b, parity) : try_wait_cta(b, parity))) return true;
         if ((i & 63) == 63) {
             if (__any_sync(0xffffffffu, *(volatile int*)abort)) return false;

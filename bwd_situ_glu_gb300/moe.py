@@ -48,6 +48,7 @@ def declare(lib):
             ("situ_linear_act_bwd", [vp, vp, cint, vp, i64, vp, vp, vp, i64, i64, i64, vp], cint),
             ("situ_linear_dgrad", [vp, vp, vp, i64, vp, vp, i64, i64, i64, vp], cint),
             ("situ_linear_wgrad_workspace", [i64, i64, i64, i64], i64),
+            ("situ_linear_selftest_wait_timeout", [vp, vp, vp], cint),
             ("situ_linear_wgrad", [vp, vp, vp, i64, vp, cint, vp, i64, vp, i64, i64, i64, vp], cint)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ret
@@ -340,6 +341,18 @@ def situ_linear_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, dw_dt
         _check(lib.situ_linear_wgrad(dz.data_ptr(), a.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"), _ptr(ws), nb,
                                      _ptr(status), R, N, K, s))
     return da, dw, dbias
+
+
+def selftest_wait_timeout(status, elapsed_ns=None, stream=None):
+    """Launch the self-test of the linear operator's bounded waits: after ~2 s it writes 1 to ``status`` (int32 [1]
+    on the device, zeroed by the caller); ``elapsed_ns`` (int64 [1]) receives the wait's duration."""
+    _sg._need(status, _I32, (1,), "status")
+    dev = status.device
+    if elapsed_ns is not None:
+        _need(elapsed_ns, _I64, (1,), dev, "elapsed_ns")
+    if stream is not None or dev.index != _device_now():
+        return _elsewhere(stream, status, lambda: selftest_wait_timeout(status, elapsed_ns))
+    _check(_lib().situ_linear_selftest_wait_timeout(status.data_ptr(), _ptr(elapsed_ns), _raw_stream(dev.index)))
 
 
 # ---------------------------------------------------------------- autograd operators

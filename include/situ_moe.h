@@ -118,6 +118,11 @@ int situ_linear_wgrad(const void* dz, const void* a, const int64_t* expert_offse
                       void* workspace, int64_t workspace_bytes, int* status, int64_t R, int64_t N, int64_t K,
                       cudaStream_t stream);
 
+/* Self-test of the failure path of the linear operator's waits (faults nothing), as
+ * situ_glu_selftest_wait_timeout: two CTAs of a cluster wait on barriers nothing completes, give up
+ * after about 2 s, write 1 to *status (device int, zeroed by the caller) and return normally. */
+int situ_linear_selftest_wait_timeout(int* status, unsigned long long* elapsed_ns, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

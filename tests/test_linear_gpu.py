@@ -343,6 +343,15 @@ def test_autograd_matches_the_calls():
         assert torch.equal(got, want)
 
 
+def test_bounded_waits_time_out_report_and_return():
+    """The pair kernels' waits run out on barriers nothing completes, say so, and leave the context usable."""
+    status, elapsed = status_word(), torch.zeros(1, dtype=torch.int64, device=DEV)
+    moe.selftest_wait_timeout(status, elapsed)
+    torch.cuda.synchronize()
+    assert status.item() == 1 and 1.5e9 <= elapsed.item() <= 20e9
+    check_fwd([200, 3], 264, 72, "none", True, False, BF, False)
+
+
 def test_refusals():
     z = lambda *s, dtype=BF: torch.zeros(s, dtype=dtype, device=DEV)  # noqa: E731
     off = torch.zeros(3, dtype=torch.int64, device=DEV)

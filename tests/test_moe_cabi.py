@@ -23,7 +23,7 @@ def lib():
 def test_every_declared_symbol_is_exported(lib):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "situ_moe.h")).read(), flags=re.S)
     names = re.findall(r"^\s*(?:int|int64_t)\s+(situ_\w+)\s*\(", text, flags=re.M)
-    assert len(names) == 13
+    assert len(names) == 14
     assert not [n for n in names if not hasattr(lib, n)]
 
 
@@ -93,6 +93,10 @@ def test_bad_arguments(lib, name, change):
 @pytest.mark.parametrize("name,change", [(n, c) for n, cs in OVER.items() for c in cs], ids=str)
 def test_overlaps(lib, name, change):
     assert getattr(lib, name)(*{**GOOD[name], **change}.values()) == OVERLAP
+
+
+def test_selftest_refusals(lib):
+    assert [lib.situ_linear_selftest_wait_timeout(*a, 0) for a in ((0, 0), (A + 2, 0), (A, B + 4))] == [INVALID] * 3
 
 
 def test_workspaces(lib):
