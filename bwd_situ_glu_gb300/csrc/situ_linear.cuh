@@ -78,19 +78,18 @@ __device__ __forceinline__ float2 act_pair(float2 z) {
 }
 
 // act'(z) in fp32.
-__device__ __forceinline__ float act_grad(int act, float z) {
-    switch (act) {
-        case SITU_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-        case SITU_ACT_SILU: {
-            const float s = 1.0f / (1.0f + __expf(-z));
-            return s * (1.0f + z * (1.0f - s));
-        }
-        case SITU_ACT_GELU: {   // Φ(z) + z·φ(z)
-            const Normal n = normal(z);
-            return fmaf(z * 0.39894228040143268f, n.e, n.cdf);
-        }
-        default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+    if constexpr (ACT == SITU_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    if constexpr (ACT == SITU_ACT_SILU) {    // σ + z·σ·(1 − σ)
+        const float s = rcp_approx(1.0f + ex2_approx(z * -1.4426950408889634f));
+        return s * fmaf(z, 1.0f - s, 1.0f);
     }
+    if constexpr (ACT == SITU_ACT_GELU) {    // Φ(z) + z·φ(z)
+        const Normal n = normal(z);
+        return fmaf(z * 0.39894228040143268f, n.e, n.cdf);
+    }
+    return 1.0f;
 }
 
 // start[1 .. E] holds counts: their inclusive prefix in place, by one warp (each lane a segment).

@@ -25,27 +25,35 @@ using namespace situ_linear;
 
 // Bias sums of 16384 rows x 3584: 28 us with the second kernel (117 MB; 17.5 us at the copy rate).
 //
-// Rows are cut into pieces of PIECE rows of one expert; a block takes a piece's 256 columns at a time
+// Rows are cut into pieces of piece_rows() rows of one expert; a block takes a piece's 256 columns at a time
 // (8 per lane, its warps take rows in turn), adds its warps' sums in order and leaves them in
 // part[piece][column]; the second kernel adds an expert's pieces in order. No result depends on timing.
-constexpr int PIECE = 128;
 constexpr int BIAS_WARPS = 8;
 constexpr int BIAS_COLS = 256;
+constexpr int MIN_PIECE = 16, MAX_PIECE = 128;
 
-int64_t max_pieces(int64_t R, int64_t E) { return R / PIECE + E; }
+// 128 rows, or fewer (two a warp at least, 64 pieces of an expert at most) until there are some four blocks an SM:
+// 461 x 1088 through silu took 28.9 us with 128.
+int64_t piece_rows(int64_t R, int64_t N, int64_t E) {
+    int64_t piece = MAX_PIECE;
+    while (piece > MIN_PIECE && (R / piece + E) * ((N + BIAS_COLS - 1) / BIAS_COLS) < 600 && R / E / piece < 32) piece /= 2;
+    return piece;
+}
 
-template <bool DZ>
+int64_t max_pieces(int64_t R, int64_t N, int64_t E) { return R / piece_rows(R, N, E) + E; }
+
+template <int ACT>
 __global__ void __launch_bounds__(BIAS_WARPS * 32)
-    act_bwd_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ pre, int act,
+    act_bwd_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ pre,
                    const int64_t* __restrict__ offsets, uint16_t* __restrict__ dz, float* __restrict__ part, int E,
-                   int64_t R, int64_t N) {
+                   int64_t R, int64_t N, int piece) {
     __shared__ int start[MAX_EXPERTS + 1];
     __shared__ float sums[BIAS_WARPS][BIAS_COLS + 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int64_t b, en;
         expert_range(offsets, e, R, b, en);
-        start[e + 1] = (int)((en - b + PIECE - 1) / PIECE);
+        start[e + 1] = (int)((en - b + piece - 1) / piece);
     }
     if (threadIdx.x == 0) start[0] = 0;
     __syncthreads();
@@ -62,8 +70,8 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
         }
         int64_t b, en;
         expert_range(offsets, lo, R, b, en);
-        const int64_t r0 = b + (int64_t)(t - start[lo]) * PIECE;
-        const int64_t r1 = min(en, r0 + PIECE);
+        const int64_t r0 = b + (int64_t)(t - start[lo]) * piece;
+        const int64_t r1 = min(en, r0 + piece);
         float s[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = 0.0f;
@@ -77,13 +85,13 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
                     f[2 * i] = bf16_lo(g.w[i]);
                     f[2 * i + 1] = bf16_hi(g.w[i]);
                 }
-                if constexpr (DZ) {
+                if constexpr (ACT != SITU_ACT_NONE) {
                     const Vec<4> z = ld_stream<4, true>((const Vec<4>*)(pre + r * N + col));
                     Vec<4> o;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        f[2 * i] *= act_grad(act, bf16_lo(z.w[i]));
-                        f[2 * i + 1] *= act_grad(act, bf16_hi(z.w[i]));
+                        f[2 * i] *= act_grad<ACT>(bf16_lo(z.w[i]));
+                        f[2 * i + 1] *= act_grad<ACT>(bf16_hi(z.w[i]));
                         o.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
                     }
                     st_stream<4>((Vec<4>*)(dz + r * N + col), o);
@@ -111,14 +119,14 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
 // blockIdx.y: expert; blockIdx.x: 256 columns.
 __global__ void __launch_bounds__(BIAS_COLS)
     bias_sum_kernel(const float* __restrict__ part, const int64_t* __restrict__ offsets, float* __restrict__ dbias,
-                    int64_t R, int64_t N) {
+                    int64_t R, int64_t N, int piece) {
     const int e = blockIdx.y, lane = threadIdx.x & 31;
     __shared__ int s_first[BIAS_COLS / 32];
     int first = 0;                           // pieces of the experts before e
     for (int i = threadIdx.x; i < e; i += blockDim.x) {
         int64_t b, en;
         expert_range(offsets, i, R, b, en);
-        first += (int)((en - b + PIECE - 1) / PIECE);
+        first += (int)((en - b + piece - 1) / piece);
     }
     first = (int)__reduce_add_sync(FULL_MASK, (unsigned)first);
     if (lane == 0) s_first[threadIdx.x >> 5] = first;
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(BIAS_COLS)
     for (int i = 0; i < BIAS_COLS / 32; ++i) first += s_first[i];
     int64_t b, en;
     expert_range(offsets, e, R, b, en);
-    const int64_t n = (en - b + PIECE - 1) / PIECE;
+    const int64_t n = (en - b + piece - 1) / piece;
     const int64_t c = (int64_t)blockIdx.x * BIAS_COLS + threadIdx.x;
     if (c >= N) return;
     float v = 0.0f;
@@ -451,7 +459,7 @@ extern "C" {
 
 int64_t situ_linear_act_bwd_workspace(int64_t R, int64_t N, int64_t E) {
     if (check_linear(E, (const void*)8, R, N, 8) != SITU_GLU_OK) return 0;
-    return max_pieces(R, E) * N * 4;
+    return max_pieces(R, N, E) * N * 4;
 }
 
 int situ_linear_act_bwd(const void* dout, const void* pre, int act, const int64_t* expert_offsets, int64_t E, void* dz,
@@ -461,6 +469,7 @@ int situ_linear_act_bwd(const void* dout, const void* pre, int act, const int64_
     if (st != SITU_GLU_OK) return st;
     if (act < SITU_ACT_NONE || act > SITU_ACT_GELU) return SITU_GLU_INVALID_ARG;
     const bool with_dz = act != SITU_ACT_NONE;
+    const int piece = (int)piece_rows(R, N, E);
     const int64_t need = dbias ? situ_linear_act_bwd_workspace(R, N, E) : 0;
     if (R > 0 && (!dout || (with_dz && (!pre || !dz)))) return SITU_GLU_INVALID_ARG;
     if (dbias && (workspace_bytes < need || !workspace)) return SITU_GLU_INVALID_ARG;
@@ -478,21 +487,22 @@ int situ_linear_act_bwd(const void* dout, const void* pre, int act, const int64_
             if (overlap(o[i], o[j])) return SITU_GLU_OVERLAP;
     }
     if (R > 0 && (with_dz || dbias)) {
-        auto kernel = with_dz ? act_bwd_kernel<true> : act_bwd_kernel<false>;
+        auto kernel = act == SITU_ACT_RELU ? act_bwd_kernel<SITU_ACT_RELU> : act == SITU_ACT_SILU ? act_bwd_kernel<SITU_ACT_SILU>
+                      : act == SITU_ACT_GELU ? act_bwd_kernel<SITU_ACT_GELU> : act_bwd_kernel<SITU_ACT_NONE>;
         int grid = 0;
-        const int64_t items = max_pieces(R, E) * ((N + BIAS_COLS - 1) / BIAS_COLS);
+        const int64_t items = max_pieces(R, N, E) * ((N + BIAS_COLS - 1) / BIAS_COLS);
         st = grid_for((const void*)kernel, BIAS_WARPS * 32, items * BIAS_WARPS, &grid);
         if (st != SITU_GLU_OK) return st;
         // several blocks a place: the pieces are short and uneven
         if ((int64_t)grid * 4 < items) grid *= 4; else grid = (int)items;
-        kernel<<<grid, BIAS_WARPS * 32, 0, stream>>>((const uint16_t*)dout, (const uint16_t*)pre, act, expert_offsets,
-                                                     (uint16_t*)dz, dbias ? (float*)workspace : nullptr, (int)E, R, N);
+        kernel<<<grid, BIAS_WARPS * 32, 0, stream>>>((const uint16_t*)dout, (const uint16_t*)pre, expert_offsets,
+                                                     (uint16_t*)dz, dbias ? (float*)workspace : nullptr, (int)E, R, N, piece);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e);
     }
     if (dbias) {
         bias_sum_kernel<<<dim3((unsigned)((N + BIAS_COLS - 1) / BIAS_COLS), (unsigned)E), BIAS_COLS, 0, stream>>>(
-            (const float*)workspace, expert_offsets, dbias, R, N);
+            (const float*)workspace, expert_offsets, dbias, R, N, piece);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e);
     }
