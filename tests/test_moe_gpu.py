@@ -376,6 +376,14 @@ def test_another_stream(raw):
     assert torch.equal(ids, ids0) and torch.equal(p, p0) and torch.equal(y, y0)
 
 
+def test_default_stream_handle():
+    """Handle 0 is the legacy default stream, as everywhere in the library."""
+    x = torch.randn(5, 40, device=DEV)
+    for a, b in zip(sg.situ_route_topk(x, 3, stream=0), sg.situ_route_topk(x, 3)):
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
+
+
 def test_autograd_matches_the_calls():
     """moe.route_topk / moe_dispatch / moe_combine: gradients flow through a routed identity layer like the
     float64 chain of the same choices."""

@@ -58,6 +58,34 @@ def test_layer_matches_autograd(T, D, H, E, K):
 
 
 @pytest.mark.gpu
+def test_step_in_a_graph():
+    """Nothing in a step waits for the host: forward and backward are captured and replayed on new inputs."""
+    layer = example().MoELayer(128, 64, 16, 4, seed=5)
+    g = torch.Generator().manual_seed(5)
+    new = lambda: torch.randn(300, 128, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    x, dy = new(), new()
+
+    def step():
+        y = layer.forward(x)
+        return dict(y=y, **layer.backward(dy))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    x.copy_(new())
+    dy.copy_(new())
+    graph.replay()
+    torch.cuda.synchronize()
+    for name, want in step().items():
+        assert torch.equal(out[name], want), name
+
+
+@pytest.mark.gpu
 def test_example_runs():
     out = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "moe_layer.py"), "--tokens", "64", "--width", "256", "--hidden",
                           "128", "--experts", "8", "--top-k", "2"], capture_output=True, text=True, timeout=300)
