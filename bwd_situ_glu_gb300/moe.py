@@ -417,6 +417,8 @@ def _autograd():
         def backward(ctx, dout):
             a, w, expert_offsets, pre = ctx.saved_tensors
             need = ctx.needs_input_grad
+            if not any(need[:3]):      # the residual's alone: no pre was kept
+                return None, None, None, dout, None, None
             dout = dout.contiguous()
             da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=_BF16,
                                          bias=need[2], need_da=need[0], need_dw=need[1])

@@ -343,6 +343,24 @@ def test_autograd_matches_the_calls():
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("needed", [(0,), (1,), (2,), (3,), (0, 3), (1, 2)])
+def test_autograd_of_some_inputs(needed, act):
+    """Gradients of some of a, w, bias, residual are those of all four, and only they are given."""
+    g = gen(14)
+    R, N, K = 37, 72, 48
+    data = [torch.randn(R, K, generator=g).to(BF), (torch.randn(N, K, generator=g) / 7).to(BF), torch.randn(N, generator=g),
+            torch.randn(R, N, generator=g).to(BF)]
+    dout = torch.randn(R, N, generator=g).to(BF).to(DEV)
+    grads = []
+    for some in ((0, 1, 2, 3), needed):
+        ins = [t.to(DEV).requires_grad_(i in some) for i, t in enumerate(data)]
+        moe.linear(*ins, act=act).backward(dout)
+        grads.append([t.grad for t in ins])
+    for i, (every, some) in enumerate(zip(*grads)):
+        assert torch.equal(some, every) if i in needed else some is None
+
+
 def test_bounded_waits_time_out_report_and_return():
     """The pair kernels' waits run out on barriers nothing completes, say so, and leave the context usable."""
     status, elapsed = status_word(), torch.zeros(1, dtype=torch.int64, device=DEV)
