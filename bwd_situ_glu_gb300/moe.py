@@ -400,8 +400,11 @@ def _autograd():
         @staticmethod
         def backward(ctx, dy):
             o, weights, row_of, expert_offsets = ctx.saved_tensors
+            plain = weights is None    # a sum: the weights are ones without a gradient
+            if plain:
+                weights = torch.ones(row_of.shape, dtype=_F32, device=o.device)
             do, dw = situ_combine_bwd(dy.contiguous(), o, row_of, weights, expert_offsets)
-            return do, dw, dy if ctx.needs_input_grad[2] else None, None, None
+            return do, None if plain else dw, dy if ctx.needs_input_grad[2] else None, None, None
 
     class Linear(torch.autograd.Function):
         @staticmethod
@@ -439,7 +442,7 @@ def moe_dispatch(x, row_of, expert_offsets):
 
 
 def moe_combine(o, weights, row_of, expert_offsets, residual=None):
-    """situ_combine, differentiable in o, weights and residual."""
+    """situ_combine, differentiable in o, weights (None: all 1) and residual."""
     return _autograd()[2].apply(o, weights, residual, row_of, expert_offsets)
 
 

@@ -406,6 +406,22 @@ def test_autograd_matches_the_calls():
     ref.near(lg.grad, ld.grad.numpy(), 60 * ref.U24 * 2 * D + 1e-5, "dlogits")
 
 
+def test_autograd_combine_without_weights():
+    """The plain sum's gradient is dy at every row of a token, zero at the rows of none."""
+    ids = torch.tensor([[0, 2], [1, -1], [2, 0]], dtype=torch.int32, device=DEV)
+    offsets, row_of, src, _ = sg.situ_dispatch_plan(ids, 3)
+    o = torch.randn(6, 24, generator=gen(10)).to(DEV).requires_grad_()
+    dy = torch.randn(3, 24, generator=gen(11)).to(DEV)
+    y = moe.moe_combine(o, None, row_of, offsets)
+    assert torch.equal(y, sg.situ_combine(o.detach(), row_of))
+    y.backward(dy)
+    want = torch.zeros_like(dy[:1]).repeat(6, 1)
+    for r, s in enumerate(src.tolist()):
+        if s >= 0:
+            want[r] = dy[s // 2]
+    assert torch.equal(o.grad, want)
+
+
 def test_refusals():
     f = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device=DEV)  # noqa: E731
     i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)  # noqa: E731
