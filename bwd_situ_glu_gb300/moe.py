@@ -366,6 +366,21 @@ def _autograd():
     if _functions is not None:
         return _functions
 
+    class Once(torch.autograd.Function):
+        """The first n of its arguments; what depends on the arguments through them has no derivative here."""
+        @staticmethod
+        def forward(ctx, n, *args):
+            return tuple(None if t is None else t.view_as(t) for t in args[:n])
+
+        @staticmethod
+        def backward(ctx, *grads):
+            raise RuntimeError("the gradients of the routing, dispatch, combine and linear operators are not "
+                               "differentiable themselves")
+
+    def once(grads, *inputs):
+        """The gradients, which depend on inputs: where a graph of them is made, a second derivative raises."""
+        return Once.apply(len(grads), *grads, *inputs) if torch.is_grad_enabled() else grads
+
     class RouteTopk(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logits, k):
@@ -378,7 +393,7 @@ def _autograd():
         @staticmethod
         def backward(ctx, dp, _):
             p, ids = ctx.saved_tensors
-            return situ_route_topk_bwd(ids, p, dp.contiguous(), ctx.experts, dtype=ctx.dtype), None
+            return *once((situ_route_topk_bwd(ids, p, dp.contiguous(), ctx.experts, dtype=ctx.dtype),), p, dp), None
 
     class Dispatch(torch.autograd.Function):
         @staticmethod
@@ -389,7 +404,7 @@ def _autograd():
         @staticmethod
         def backward(ctx, dh):
             (row_of,) = ctx.saved_tensors
-            return situ_combine(dh.contiguous(), row_of), None, None
+            return *once((situ_combine(dh.contiguous(), row_of),), dh), None, None
 
     class Combine(torch.autograd.Function):
         @staticmethod
@@ -404,7 +419,8 @@ def _autograd():
             if plain:
                 weights = torch.ones(row_of.shape, dtype=_F32, device=o.device)
             do, dw = situ_combine_bwd(dy.contiguous(), o, row_of, weights, expert_offsets)
-            return do, None if plain else dw, dy if ctx.needs_input_grad[2] else None, None, None
+            do, dw = once((do, None if plain else dw), dy, o, weights)
+            return do, dw, dy if ctx.needs_input_grad[2] else None, None, None
 
     class Linear(torch.autograd.Function):
         @staticmethod
@@ -412,19 +428,20 @@ def _autograd():
             keep = act != "none" and any(ctx.needs_input_grad[:3])
             out = situ_linear(a, w, expert_offsets, bias, residual, act, save_pre=keep)
             out, pre = out if keep else (out, None)
-            ctx.save_for_backward(a, w, expert_offsets, pre)
+            ctx.save_for_backward(a, w, expert_offsets, pre, bias if keep else None)
             ctx.act = act
             return out
 
         @staticmethod
         def backward(ctx, dout):
-            a, w, expert_offsets, pre = ctx.saved_tensors
+            a, w, expert_offsets, pre, bias = ctx.saved_tensors
             need = ctx.needs_input_grad
             if not any(need[:3]):      # the residual's alone: no pre was kept
                 return None, None, None, dout, None, None
             dout = dout.contiguous()
             da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=_BF16,
                                          bias=need[2], need_da=need[0], need_dw=need[1])
+            da, dw, db = once((da, dw, db), dout, a, w, bias)
             return da, dw, db, dout if need[3] else None, None, None
 
     _functions = (RouteTopk, Dispatch, Combine, Linear)

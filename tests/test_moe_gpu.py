@@ -422,6 +422,31 @@ def test_autograd_combine_without_weights():
     assert torch.equal(o.grad, want)
 
 
+@pytest.mark.parametrize("constant", [False, True])
+@pytest.mark.parametrize("op", ["route", "dispatch", "combine", "linear"])
+def test_second_derivatives_are_refused(op, constant):
+    """The gradients are kernels without a derivative of their own: differentiating them raises, it does not
+    give zeros."""
+    g = gen(12)
+    x = torch.randn(4, 16, generator=g).to(DEV)
+    offsets, row_of, _, _ = sg.situ_dispatch_plan(torch.tensor([[0], [2], [1], [2]], dtype=torch.int32, device=DEV), 3)
+    p = torch.rand(4, 1, generator=g).to(DEV)
+    if op == "linear":
+        x = x.to(torch.bfloat16)
+    x.requires_grad_()
+    out = {"route": lambda: moe.route_topk(x, 2)[0], "dispatch": lambda: moe.moe_dispatch(x, row_of, offsets),
+           "combine": lambda: moe.moe_combine(x, p.requires_grad_(), row_of, offsets),
+           "linear": lambda: moe.linear(x, torch.ones(8, 16, dtype=torch.bfloat16, device=DEV), act="silu")}[op]()
+    scale = torch.rand(out.shape, generator=g).to(DEV, out.dtype).requires_grad_(not constant)
+    (dx,) = torch.autograd.grad(out, x, scale, create_graph=True)
+    if op == "dispatch" and constant:      # linear: the gradient does not depend on x
+        (dx * x).sum().backward()
+        assert torch.equal(x.grad, dx)
+        return
+    with pytest.raises(RuntimeError):
+        (dx * x).sum().backward()
+
+
 def test_refusals():
     f = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device=DEV)  # noqa: E731
     i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)  # noqa: E731
