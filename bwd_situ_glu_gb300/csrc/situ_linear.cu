@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int NT = (int)((NCOL + TILE - 1) / TILE);
     const int sbytes = stage_bytes(most), stages = ring_stages(most);
 
+    const bool orderly = offsets_orderly(offsets, E, R);
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int64_t b, en;
-        expert_range(offsets, e, R, b, en);
+        rows_of_expert(offsets, e, R, orderly, b, en);
         plan.begin[e] = (int)b;
         plan.rows[e] = (int)(en - b);
         plan.start[e + 1] = (int)((en - b + most - 1) / most);
@@ -456,9 +457,10 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
     __shared__ int tile_start[MAX_EXPERTS + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // first job of each expert: ceil(rows / FEW_ROWS) each
+    const bool orderly = offsets_orderly(offsets, E, R);
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int64_t b, en;
-        expert_range(offsets, e, R, b, en);
+        rows_of_expert(offsets, e, R, orderly, b, en);
         tile_start[e + 1] = (int)((en - b + FEW_ROWS - 1) / FEW_ROWS);
     }
     if (threadIdx.x == 0) tile_start[0] = 0;
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
             if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
         }
         int64_t b, en;
-        expert_range(offsets, lo, R, b, en);
+        rows_of_expert(offsets, lo, R, orderly, b, en);
         const int64_t row0 = b + (int64_t)(t - tile_start[lo]) * FEW_ROWS;
         const int rows = (int)min((int64_t)FEW_ROWS, en - row0);
         const uint16_t* we = w + (int64_t)lo * N * K;

@@ -50,9 +50,10 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
     __shared__ int start[MAX_EXPERTS + 1];
     __shared__ float sums[BIAS_WARPS][BIAS_COLS + 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool orderly = offsets_orderly(offsets, E, R);
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int64_t b, en;
-        expert_range(offsets, e, R, b, en);
+        rows_of_expert(offsets, e, R, orderly, b, en);
         start[e + 1] = (int)((en - b + piece - 1) / piece);
     }
     if (threadIdx.x == 0) start[0] = 0;
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
             if (start[mid] <= t) lo = mid; else hi = mid - 1;
         }
         int64_t b, en;
-        expert_range(offsets, lo, R, b, en);
+        rows_of_expert(offsets, lo, R, orderly, b, en);
         const int64_t r0 = b + (int64_t)(t - start[lo]) * piece;
         const int64_t r1 = min(en, r0 + piece);
         float s[8];
@@ -122,10 +123,11 @@ __global__ void __launch_bounds__(BIAS_COLS)
                     int64_t R, int64_t N, int piece) {
     const int e = blockIdx.y, lane = threadIdx.x & 31;
     __shared__ int s_first[BIAS_COLS / 32];
+    const bool orderly = offsets_orderly(offsets, (int)gridDim.y, R);
     int first = 0;                           // pieces of the experts before e
     for (int i = threadIdx.x; i < e; i += blockDim.x) {
         int64_t b, en;
-        expert_range(offsets, i, R, b, en);
+        rows_of_expert(offsets, i, R, orderly, b, en);
         first += (int)((en - b + piece - 1) / piece);
     }
     first = (int)__reduce_add_sync(FULL_MASK, (unsigned)first);
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(BIAS_COLS)
 #pragma unroll
     for (int i = 0; i < BIAS_COLS / 32; ++i) first += s_first[i];
     int64_t b, en;
-    expert_range(offsets, e, R, b, en);
+    rows_of_expert(offsets, e, R, orderly, b, en);
     const int64_t n = (en - b + piece - 1) / piece;
     const int64_t c = (int64_t)blockIdx.x * BIAS_COLS + threadIdx.x;
     if (c >= N) return;
@@ -237,9 +239,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int jobs = E * splits * MT * NT;
     const int j0 = blockIdx.x >> 1, jstep = gridDim.x >> 1;
 
+    const bool orderly = offsets_orderly(offsets, E, R);
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int64_t b, en;
-        expert_range(offsets, e, R, b, en);
+        rows_of_expert(offsets, e, R, orderly, b, en);
         plan.begin[e] = (int)b;
         plan.rows[e] = (int)(en - b);
     }
