@@ -7,7 +7,6 @@
 
 #include "../../include/situ_moe.h"
 #include "situ_host.h"
-#include "situ_tc.cuh"
 
 namespace situ_linear {
 
@@ -91,30 +90,6 @@ __device__ __forceinline__ float act_grad(float z) {
         return fmaf(z * 0.39894228040143268f, n.e, n.cdf);
     }
     return 1.0f;
-}
-
-// Whether the offsets run from 0 to R at most without decreasing; for all threads of a block, which meet here. (Without
-// offsets, the dense products, they do.)
-__device__ __forceinline__ bool offsets_orderly(const int64_t* off, int E, int64_t R) {
-    if (!off) return true;
-    bool ok = true;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) ok = ok && off[e] >= 0 && off[e] <= off[e + 1] && off[e + 1] <= R;
-    return __syncthreads_and(ok) != 0;
-}
-
-// Expert e's rows [begin, end) within [0, R]. Out-of-order offsets are read as the largest one so far, so that no
-// row has two experts: the work lists and workspaces hold R rows' worth of pieces and one more an expert. That reading
-// walks the offsets before e, which orderly ones are spared.
-__device__ __forceinline__ void rows_of_expert(const int64_t* off, int e, int64_t R, bool orderly, int64_t& begin,
-                                               int64_t& end) {
-    if (orderly) {
-        situ_tc::expert_range(off, e, R, begin, end);
-        return;
-    }
-    int64_t most = 0;
-    for (int i = 0; i <= e; ++i) most = max(most, min(off[i], R));
-    begin = most;
-    end = max(most, min(off[e + 1], R));
 }
 
 // start[1 .. E] holds counts: their inclusive prefix in place, by one warp (each lane a segment).

@@ -363,9 +363,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* b, uint32_t parity, 
 // Named barrier over the epilogue warps only (id 1; id 0 is __syncthreads).
 __device__ __forceinline__ void epi_barrier(int nthreads) { asm volatile("bar.sync 1, %0;" ::"r"(nthreads) : "memory"); }
 
-// Expert e's rows as [begin, end) clamped into [0, R] (end >= begin): malformed offsets can
-// neither index outside the row range nor inflate the number of tiles beyond R/BM + E. Without
-// offsets (the dense products) the one expert owns every row.
+// Expert e's rows as [begin, end) clamped into [0, R] (end >= begin): malformed offsets cannot index
+// outside the row range. They can give a row to several experts, so counts of tiles or pieces over
+// the experts go by rows_of_expert. Without offsets (the dense products) the one expert owns every row.
 __device__ __forceinline__ void expert_range(const int64_t* off, int e, int64_t R, int64_t& begin, int64_t& end) {
     if (!off) {
         begin = 0;
@@ -379,7 +379,32 @@ __device__ __forceinline__ void expert_range(const int64_t* off, int e, int64_t 
     end = b;
 }
 
-// M-tile t -> (expert, first row, end row of the expert).
+// Whether the offsets run from 0 to R at most without decreasing; for all threads of a block, which meet here. (Without
+// offsets, the dense products, they do.)
+__device__ __forceinline__ bool offsets_orderly(const int64_t* off, int E, int64_t R) {
+    if (!off) return true;
+    bool ok = true;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) ok = ok && off[e] >= 0 && off[e] <= off[e + 1] && off[e + 1] <= R;
+    return __syncthreads_and(ok) != 0;
+}
+
+// Expert e's rows [begin, end) within [0, R]. Out-of-order offsets are read as the largest one so far, so that no
+// row has two experts: the work lists and workspaces hold R rows' worth of pieces and one more an expert. That reading
+// walks the offsets before e, which orderly ones are spared.
+__device__ __forceinline__ void rows_of_expert(const int64_t* off, int e, int64_t R, bool orderly, int64_t& begin,
+                                               int64_t& end) {
+    if (orderly) {
+        expert_range(off, e, R, begin, end);
+        return;
+    }
+    int64_t most = 0;
+    for (int i = 0; i <= e; ++i) most = max(most, min(off[i], R));
+    begin = most;
+    end = max(most, min(off[e + 1], R));
+}
+
+// M-tile t -> (expert, first row, end row of the expert). With out-of-order offsets the counts in tile_start are at most
+// those of the clamped range, so the tile lies inside it.
 __device__ __forceinline__ void tile_rows(const int* tile_start, const int64_t* off, int E, int64_t R, int t,
                                           int& e, int64_t& row0, int64_t& row_end) {
     int lo = 0, hi = E - 1;                 // last e with tile_start[e] <= t
@@ -440,9 +465,10 @@ __device__ __forceinline__ int pipeline_setup(const Smem& sm, const int64_t* off
     Barriers* bars = sm.bars;
     int* tile_start = sm.tile_start;             // per expert: its first work unit
     const int64_t unit_rows = (int64_t)unit_tiles * BM;
+    const bool orderly = offsets_orderly(offsets, E, R);
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int64_t begin, end;
-        expert_range(offsets, e, R, begin, end);
+        rows_of_expert(offsets, e, R, orderly, begin, end);
         tile_start[e + 1] = (int)((end - begin + unit_rows - 1) / unit_rows);
     }
     if (threadIdx.x == 0) {

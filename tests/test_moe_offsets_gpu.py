@@ -115,3 +115,36 @@ def test_dispatch_and_combine(name):
     want = torch.einsum("td,tkd->tk", x.double(), o.double()[row_of.long()])     # does not depend on the offsets
     # some 20 fp32 additions in a chain, of products whose absolute values sum to less than 80
     assert (dp.view(torch.float32, T, K).double() - want).abs().max() < 20 * 2.0 ** -24 * 80
+
+
+@pytest.mark.parametrize("call", ["gateup", "dgrad"])
+def test_fused_products_stay_bounded(call):
+    """Overlapping offsets are no more work for the fused products than orderly ones over the same rows (ceil(R/128) + E
+    row tiles; every second expert owning every row would be 300 times that)."""
+    R, H, D, E = 100_000, 256, 64, 1023
+    g = torch.Generator(device=DEV).manual_seed(5)
+    new = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)  # noqa: E731
+    h, w, x, p = new(R, D), new(E, 2 * H, D), new(R, 2 * H), torch.rand(R, generator=g, device=DEV)
+    xo, out, dx = Guarded(R * 2 * H * 2), Guarded(R * H * 2), Guarded(R * 2 * H * 2)
+    dp = torch.empty(R, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def ms(off):
+        best = []
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            if call == "gateup":
+                sg.situ_glu_fwd_gateup(h, w, off, xo.view(BF, R, 2 * H), out.view(BF, R, H), status=st)
+            else:
+                sg.situ_glu_bwd_router_dgrad(x, h, w[:, :H].contiguous(), off, p, dx.view(BF, R, 2 * H), dp, status=st)
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b))
+        return min(best)
+
+    orderly = torch.linspace(0, R, E + 1, device=DEV).long()
+    overlapping = torch.tensor([0, R] * 512, device=DEV)
+    t = ms(orderly), ms(overlapping)
+    assert st.item() == 0
+    assert t[1] < 5 * t[0], t
