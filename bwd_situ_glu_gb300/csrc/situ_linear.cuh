@@ -120,9 +120,11 @@ inline int sm_count(int* sms) {
     return e == cudaSuccess ? SITU_GLU_OK : situ_host::cuda_fail(e);
 }
 
-// Sizes shared by the product and its gradients.
+// Sizes shared by the product and its gradients. Row numbers are 32-bit, those past the last row that a chunk rounded up
+// (32 rows) or the end of a split contraction (at most 16 blocks of 64) reaches among them.
+constexpr int64_t MAX_ROWS = INT32_MAX - 1024;
 inline int check_linear(int64_t E, const void* offsets, int64_t R, int64_t N, int64_t K) {
-    if (R < 0 || R > INT32_MAX || N < 8 || N % 8 != 0 || K < 8 || K % 8 != 0 || E < 1 || E > SITU_MAX_EXPERTS)
+    if (R < 0 || R > MAX_ROWS || N < 8 || N % 8 != 0 || K < 8 || K % 8 != 0 || E < 1 || E > SITU_MAX_EXPERTS)
         return SITU_GLU_INVALID_ARG;
     if (N > INT32_MAX / 4 || K > INT32_MAX / 4 || E * N > INT32_MAX || E * K > INT32_MAX) return SITU_GLU_INVALID_ARG;
     if (!offsets && E != 1) return SITU_GLU_INVALID_ARG;

@@ -93,7 +93,7 @@ int situ_combine_bwd(const void* dy, const void* o, int type, const int32_t* row
  * layout), bias fp32 [E, N] or NULL, residual bf16 [R, N] or NULL, out [R, N] of out_type, pre bf16
  * [R, N] or NULL (receives z rounded to bf16, what the backward reads). expert_offsets int64 [E+1],
  * or NULL with E = 1: one weight for all rows. Rows outside every expert's range are not written.
- * N % 8 == 0, K % 8 == 0; 1 <= E <= 1024; a, w, residual, out and pre 16-byte aligned. status
+ * N % 8 == 0, K % 8 == 0; 1 <= E <= 1024; R <= 2^31 - 1025; a, w, residual, out and pre 16-byte aligned. status
  * (device int, zeroed by the caller, may be NULL) turns 1 if a pipeline wait timed out. */
 int situ_linear_fwd(const void* a, const void* w, const int64_t* expert_offsets, int64_t E, const float* bias,
                     const void* residual, int act, void* out, int out_type, void* pre, int* status, int64_t R,
