@@ -150,10 +150,31 @@ def load():
     lib.situ_glu_last_cuda_error.restype = cint
     lib.situ_glu_version.argtypes = []
     lib.situ_glu_version.restype = cint
-    from . import moe
-    moe.declare(lib)
+    _declare_moe(lib)
     _lib = lib
     return lib
+
+
+def _declare_moe(lib):
+    """ctypes signatures of include/situ_moe.h; here, so that loading the library does not import torch."""
+    vp, i64, cint = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    for name, args, ret in (
+            ("situ_route_topk", [vp, cint, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_route_topk_bwd", [vp, vp, vp, vp, i64, vp, cint, i64, i64, i64, vp], cint),
+            ("situ_dispatch_plan_workspace", [i64, i64, i64], i64),
+            ("situ_dispatch_plan", [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_dispatch", [vp, cint, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_combine", [vp, cint, vp, vp, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_combine_bwd", [vp, vp, cint, vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp], cint),
+            ("situ_linear_fwd", [vp, vp, vp, i64, vp, vp, cint, vp, cint, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_linear_act_bwd_workspace", [i64, i64, i64], i64),
+            ("situ_linear_act_bwd", [vp, vp, cint, vp, i64, vp, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_linear_dgrad", [vp, vp, vp, i64, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_linear_wgrad_workspace", [i64, i64, i64, i64], i64),
+            ("situ_linear_selftest_wait_timeout", [vp, vp, vp], cint),
+            ("situ_linear_wgrad", [vp, vp, vp, i64, vp, cint, vp, i64, vp, i64, i64, i64, vp], cint)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ret
 
 
 def status_string(status: int) -> str:

@@ -14,8 +14,6 @@ workspaces are allocated on that stream.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 import bwd_situ_glu_gb300 as _sg
@@ -30,28 +28,6 @@ _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRa
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 MAX_EXPERTS, MAX_TOPK = 1024, 32  # SITU_MAX_EXPERTS, SITU_MAX_TOPK
-
-
-def declare(lib):
-    """ctypes signatures of include/situ_moe.h (called once by load())."""
-    vp, i64, cint = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
-    for name, args, ret in (
-            ("situ_route_topk", [vp, cint, vp, vp, i64, i64, i64, vp], cint),
-            ("situ_route_topk_bwd", [vp, vp, vp, vp, i64, vp, cint, i64, i64, i64, vp], cint),
-            ("situ_dispatch_plan_workspace", [i64, i64, i64], i64),
-            ("situ_dispatch_plan", [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp], cint),
-            ("situ_dispatch", [vp, cint, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp], cint),
-            ("situ_combine", [vp, cint, vp, vp, vp, vp, i64, i64, i64, i64, vp], cint),
-            ("situ_combine_bwd", [vp, vp, cint, vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp], cint),
-            ("situ_linear_fwd", [vp, vp, vp, i64, vp, vp, cint, vp, cint, vp, vp, i64, i64, i64, vp], cint),
-            ("situ_linear_act_bwd_workspace", [i64, i64, i64], i64),
-            ("situ_linear_act_bwd", [vp, vp, cint, vp, i64, vp, vp, vp, i64, i64, i64, vp], cint),
-            ("situ_linear_dgrad", [vp, vp, vp, i64, vp, vp, i64, i64, i64, vp], cint),
-            ("situ_linear_wgrad_workspace", [i64, i64, i64, i64], i64),
-            ("situ_linear_selftest_wait_timeout", [vp, vp, vp], cint),
-            ("situ_linear_wgrad", [vp, vp, vp, i64, vp, cint, vp, i64, vp, i64, i64, i64, vp], cint)):
-        fn = getattr(lib, name)
-        fn.argtypes, fn.restype = args, ret
 
 
 def _type(t, name):
