@@ -30,6 +30,7 @@ Shapes: ``x`` bf16 [R, 2H] (gate | linear), ``g`` bf16 [R, H], ``p`` fp32 [R];
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import subprocess
 import threading
@@ -539,7 +540,6 @@ _MOE_NAMES = ("situ_route_topk", "situ_route_topk_bwd", "situ_dispatch_plan", "s
 def __getattr__(name):
     """The operators around the activation live in the module ``moe``, which imports torch: on first use."""
     if name == "moe" or name in _MOE_NAMES:
-        import importlib
         m = importlib.import_module(__name__ + ".moe")
         globals().update({n: getattr(m, n) for n in _MOE_NAMES}, moe=m)
         return globals()[name]
@@ -552,6 +552,7 @@ __all__ = [
     "situ_glu_fwd_save_fp8", "situ_glu_bwd_router_fp8", "FP8_BLOCK", "fp8_scale_blocks",
     "situ_glu_bwd_router_dgrad", "situ_glu_bwd_router_dgrad_wd", "situ_glu_fwd_gateup",
     "situ_and_mul", "selftest_wait_timeout", "AdamParams", "adam_params", "situ_adam_update_host", "situ_adam_stream_step", "adam_staging_bytes",
-    "moe", *_MOE_NAMES,
     "LIB_PATH", "INCLUDE",
 ]
+if importlib.util.find_spec("torch") is not None:   # `import *` of the rest works without torch
+    __all__ += ["moe", *_MOE_NAMES]

@@ -45,3 +45,14 @@ def test_loads_without_torch(lib):
                         "try: sg.situ_glu_fwd_ptr(0, 0, -1, 8)\n"
                         "except sg.SituGluError as e: print(e.status)")
     assert out.split() == [str(sg.version()), *sg.status_string(1).split(), "1", "1"]
+
+
+def test_star_import_without_torch():
+    assert without_torch("from bwd_situ_glu_gb300 import *\nprint(situ_glu_fwd_ptr.__name__, 'situ_linear' in globals())").split() == [
+        "situ_glu_fwd_ptr", "False"]
+
+
+def test_star_import():
+    names = {}
+    exec("from bwd_situ_glu_gb300 import *", names)
+    assert names["situ_linear"] is sg.situ_linear and names["moe"] is sg.moe and names["situ_glu_fwd"] is sg.situ_glu_fwd
