@@ -83,7 +83,7 @@ __device__ __forceinline__ Job job_at(int j, const Plan& plan, int E, int NT) {
     const int width = min(GROUP, nch - g * GROUP);
     q.nt = rem / width;
     const int c = g * GROUP + rem - q.nt * width;
-    const int size = (int)((((uint32_t)plan.rows[lo] + nch - 1) / nch + 31) & ~31u);   // the sum may pass 2^31
+    const int size = ((plan.rows[lo] - 1) / nch + 32) & ~31;   // no sum that could pass 2^31
     q.row0 = plan.begin[lo] + c * size;
     q.rows = min(size, plan.rows[lo] - c * size);
     q.n = (q.rows + 31) & ~31;
