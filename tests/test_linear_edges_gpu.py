@@ -35,3 +35,34 @@ def test_most_rows():
         assert not out[r].any() and not da[r].any()
     assert torch.equal(dw, sum(dz[r].float().t() @ a[r].float() for r in places))
     assert torch.equal(db, sum(dz[r].float().sum(0) for r in places))
+
+
+# gelu on the left side: fp32 evaluation of Φ(z) = t·P(t)·e^{-z²/2} is good to 8e-7 (the fit), some ten roundings and the
+# approximate exp2 and reciprocal (2^-22 each): below 3e-6, and the exponent z²/2 is rounded twice: z²·1.2e-7
+def gelu_rel(z):
+    return 3e-6 + z * z * 1.2e-7
+
+
+@pytest.mark.parametrize("R", [1, 256])                # streamed weights, and tiles
+def test_gelu_relative_accuracy(R):
+    """fp32 outputs down to z = -9, where gelu is -1e-18, keep their digits."""
+    N = 1024
+    z = torch.cat([-torch.linspace(0, 9, N - 8), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3.0, 9.0, 40.0, 3e38])])
+    out = sg.situ_linear(torch.zeros(R, 8, dtype=BF, device=DEV), torch.ones(N, 8, dtype=BF, device=DEV), bias=z.to(DEV), act="gelu",
+                         out_dtype=torch.float32)
+    zd = z.double().numpy()
+    want = ref.act(zd, "gelu")[0]
+    ref.near(out, np.broadcast_to(want, (R, N)), gelu_rel(np.minimum(np.abs(zd), 9)) * np.abs(want), "out")
+
+
+def test_gelu_gradient_accuracy():
+    """The bias gradient of one row is act'(pre) in fp32: Φ(z) + z·φ(z), each term to the same relative accuracy."""
+    z = torch.cat([-torch.linspace(0, 9, 1016), torch.linspace(0, 40, 8)]).to(BF)
+    N = z.numel()
+    pre = z[None].to(DEV)
+    _, _, db = sg.situ_linear_bwd(torch.ones(1, N, dtype=BF, device=DEV), None, torch.zeros(N, 8, dtype=BF, device=DEV), act="gelu",
+                                  pre=pre, need_da=False, need_dw=False)
+    zd = z.double().numpy()
+    cdf = 0.5 * torch.special.erfc(-z.double() / math.sqrt(2)).numpy()
+    zphi = np.abs(zd) * np.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+    ref.near(db, ref.act(zd, "gelu")[1], gelu_rel(np.abs(zd)) * (cdf + zphi), "dbias")
