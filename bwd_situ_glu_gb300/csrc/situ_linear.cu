@@ -161,16 +161,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int NT = (int)((NCOL + TILE - 1) / TILE);
     const int sbytes = stage_bytes(most), stages = ring_stages(most);
 
-    const bool orderly = offsets_orderly(offsets, E, R);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int64_t b, en;
-        rows_of_expert(offsets, e, R, orderly, b, en);
+    if (threadIdx.x == 0) plan.start[0] = 0;
+    const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) {
         plan.begin[e] = (int)b;
         plan.rows[e] = (int)(en - b);
         plan.start[e + 1] = (int)((en - b + most - 1) / most);
-    }
-    if (threadIdx.x == 0) plan.start[0] = 0;
-    __syncthreads();
+    });
+    if (!orderly) drop_overlapping(offsets, E, R, plan.start + 1, plan.rows);
     if (warp == 0) prefix_in_place(plan.start, E, lane);
     const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS);
     const int jobs = plan.start[E] * NT;
@@ -457,14 +454,11 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
     __shared__ int tile_start[MAX_EXPERTS + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // first job of each expert: ceil(rows / FEW_ROWS) each
-    const bool orderly = offsets_orderly(offsets, E, R);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int64_t b, en;
-        rows_of_expert(offsets, e, R, orderly, b, en);
-        tile_start[e + 1] = (int)((en - b + FEW_ROWS - 1) / FEW_ROWS);
-    }
     if (threadIdx.x == 0) tile_start[0] = 0;
-    __syncthreads();
+    const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) {
+        tile_start[e + 1] = (int)((en - b + FEW_ROWS - 1) / FEW_ROWS);
+    });
+    if (!orderly) drop_overlapping(offsets, E, R, tile_start + 1, nullptr);
     if (warp == 0) prefix_in_place(tile_start, E, lane);
     __syncthreads();
     const int T = tile_start[E];
@@ -479,7 +473,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
             if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
         }
         int64_t b, en;
-        rows_of_expert(offsets, lo, R, orderly, b, en);
+        expert_range(offsets, lo, R, b, en);
         const int64_t row0 = b + (int64_t)(t - tile_start[lo]) * FEW_ROWS;
         const int rows = (int)min((int64_t)FEW_ROWS, en - row0);
         const uint16_t* we = w + (int64_t)lo * N * K;

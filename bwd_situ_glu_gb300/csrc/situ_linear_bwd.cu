@@ -50,14 +50,11 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
     __shared__ int start[MAX_EXPERTS + 1];
     __shared__ float sums[BIAS_WARPS][BIAS_COLS + 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool orderly = offsets_orderly(offsets, E, R);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int64_t b, en;
-        rows_of_expert(offsets, e, R, orderly, b, en);
-        start[e + 1] = (int)((en - b + piece - 1) / piece);
-    }
     if (threadIdx.x == 0) start[0] = 0;
-    __syncthreads();
+    const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) {
+        start[e + 1] = (int)((en - b + piece - 1) / piece);
+    });
+    if (!orderly) drop_overlapping(offsets, E, R, start + 1, nullptr);
     if (warp == 0) prefix_in_place(start, E, lane);
     __syncthreads();
     const int64_t cb = (N + BIAS_COLS - 1) / BIAS_COLS, items = (int64_t)start[E] * cb;
@@ -70,7 +67,7 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
             if (start[mid] <= t) lo = mid; else hi = mid - 1;
         }
         int64_t b, en;
-        rows_of_expert(offsets, lo, R, orderly, b, en);
+        expert_range(offsets, lo, R, b, en);
         const int64_t r0 = b + (int64_t)(t - start[lo]) * piece;
         const int64_t r1 = min(en, r0 + piece);
         float s[8];
@@ -123,22 +120,20 @@ __global__ void __launch_bounds__(BIAS_COLS)
                     int64_t R, int64_t N, int piece) {
     const int e = blockIdx.y, lane = threadIdx.x & 31;
     __shared__ int s_first[BIAS_COLS / 32];
-    const bool orderly = offsets_orderly(offsets, (int)gridDim.y, R);
+    __shared__ int s_count[MAX_EXPERTS];
+    const bool orderly = each_expert(offsets, (int)gridDim.y, R, [&](int i, int64_t b, int64_t en) {
+        s_count[i] = (int)((en - b + piece - 1) / piece);
+    });
+    if (!orderly) drop_overlapping(offsets, (int)gridDim.y, R, s_count, nullptr);
     int first = 0;                           // pieces of the experts before e
-    for (int i = threadIdx.x; i < e; i += blockDim.x) {
-        int64_t b, en;
-        rows_of_expert(offsets, i, R, orderly, b, en);
-        first += (int)((en - b + piece - 1) / piece);
-    }
+    for (int i = threadIdx.x; i < e; i += blockDim.x) first += s_count[i];
     first = (int)__reduce_add_sync(FULL_MASK, (unsigned)first);
     if (lane == 0) s_first[threadIdx.x >> 5] = first;
     __syncthreads();
     first = 0;
 #pragma unroll
     for (int i = 0; i < BIAS_COLS / 32; ++i) first += s_first[i];
-    int64_t b, en;
-    rows_of_expert(offsets, e, R, orderly, b, en);
-    const int64_t n = (en - b + piece - 1) / piece;
+    const int64_t n = s_count[e];
     const int64_t c = (int64_t)blockIdx.x * BIAS_COLS + threadIdx.x;
     if (c >= N) return;
     float v = 0.0f;
@@ -239,13 +234,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int jobs = E * splits * MT * NT;
     const int j0 = blockIdx.x >> 1, jstep = gridDim.x >> 1;
 
-    const bool orderly = offsets_orderly(offsets, E, R);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int64_t b, en;
-        rows_of_expert(offsets, e, R, orderly, b, en);
+    const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) {
         plan.begin[e] = (int)b;
         plan.rows[e] = (int)(en - b);
-    }
+    });
+    if (!orderly) drop_overlapping(offsets, E, R, plan.rows, nullptr);
     const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS);
 
     if (warp == 0) {

@@ -18,9 +18,9 @@
  * `stream` without a host wait, every argument is checked on the host before any launch, and the
  * result is a status code (SITU_GLU_OK, _INVALID_ARG, _OVERLAP, _CUDA_ERROR). Element types are
  * SITU_BF16 or SITU_FP32 where a function takes one. expert_offsets are non-decreasing, from 0 to at
- * most R (what situ_dispatch_plan gives). Others are clamped into [0, R], and the products read each as
- * the largest one so far, so that no row has two experts: nothing is accessed outside the buffers and
- * the work stays bounded. A call without rows (T, R or the like = 0)
+ * most R (what situ_dispatch_plan gives). Others are clamped into [0, R], and in the products an expert
+ * that begins before an earlier one ends has no rows: nothing is accessed outside the buffers and the
+ * work stays bounded. A call without rows (T, R or the like = 0)
  * succeeds; outputs that do not depend on rows (gradients of weights and biases, offsets) are
  * written all the same.
  */

@@ -1,7 +1,8 @@
 """Expert offsets that are negative, decreasing, far beyond R or overlapping, given to the expert layer's operators: nothing
 outside the buffers is written (guard bands around every output and workspace, the workspaces at exactly the size the
-library asks for), the calls return promptly, and the products read the offsets as the largest one so far, clamped into
-[0, R]: bit for bit what those offsets give."""
+library asks for), the calls return promptly, and in the products every expert has the rows of its offsets clamped into
+[0, R], but none where it begins before an earlier one ends; tolerances as in test_linear_gpu.py."""
+import math
 import time
 
 import numpy as np
@@ -9,6 +10,7 @@ import pytest
 import torch
 
 import bwd_situ_glu_gb300 as sg
+import _moe_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -62,9 +64,35 @@ def ok(status):
     assert status == sg.STATUS_OK
 
 
-def everything(off, R, N, K, act):
-    """All products and gradients for these offsets, through the C entry points."""
-    lib, E = sg.load(), off.numel() - 1
+def ranges(raw, R):
+    """(begin, end) of the experts that keep rows, by expert."""
+    kept, last = {}, 0
+    for e, (a, b) in enumerate(zip(raw[:-1], raw[1:])):
+        a = min(max(a, 0), R)
+        b = min(max(b, a), R)
+        if a >= last:
+            last = b
+            if b > a:
+                kept[e] = slice(a, b)
+    return kept
+
+
+def near(got, want, tol, what):
+    assert ((got.double() - want).abs() <= tol).all(), what
+
+
+def steps_tol(n, mag):
+    return (n / 16 + 2) * 2.0 ** -22 * mag
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("name", BAD)
+@pytest.mark.parametrize("R", [40, 200, 2100])
+def test_products(R, name, act):
+    lib, N, K = sg.load(), 264, 72
+    raw = BAD[name](R)
+    E = len(raw) - 1
+    off = torch.from_numpy(np.array(raw, dtype=np.int64)).to(DEV)
     g = torch.Generator(device=DEV).manual_seed(3)
     new = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)  # noqa: E731
     a, w, dout, z, res = new(R, K), new(E, N, K), new(R, N), new(R, N), new(R, N)
@@ -86,19 +114,27 @@ def everything(off, R, N, K, act):
                              status.data_ptr(), R, N, K, s))
     torch.cuda.synchronize()
     assert status.item() == 0
-    return [out.view(BF, R, N), pre.view(BF, R, N), dz.view(BF, R, N), da.view(BF, R, K), dw.view(torch.float32, E, N, K),
-            db.view(torch.float32, E, N)]
-
-
-@pytest.mark.parametrize("act", ["none", "silu"])
-@pytest.mark.parametrize("name", BAD)
-@pytest.mark.parametrize("R", [40, 200, 2100])
-def test_products(R, name, act):
-    raw = np.array(BAD[name](R), dtype=np.int64)
-    repaired = np.maximum.accumulate(np.clip(raw, 0, R))
-    got, want = (everything(torch.from_numpy(o).to(DEV), R, 264, 72, act) for o in (raw, repaired))
-    for g, w, what in zip(got, want, ("out", "pre", "dz", "da", "dw", "dbias")):
-        assert torch.equal(g, w), what
+    # the definitions in float64; what no expert owns stays the zero that it was, and so do its gradients
+    zeros = lambda *s: torch.zeros(*s, dtype=torch.float64, device=DEV)  # noqa: E731
+    want = dict(out=zeros(R, N), pre=zeros(R, N), dz=zeros(R, N), da=zeros(R, K), dw=zeros(E, N, K), db=zeros(E, N))
+    tol = {k: v.clone() for k, v in want.items()}
+    half = 1.01 * ref.BF16_HALF
+    for e, r in ranges(raw, R).items():
+        A, W, G, Z = a[r].double(), w[e].double(), dout[r].double(), z[r].double()
+        y = A @ W.t() + bias[e]
+        mag = A.abs() @ W.abs().t() + bias[e].abs()
+        sig, y_sig = torch.sigmoid(Z), torch.sigmoid(y)
+        slope = sig * (1 + Z * (1 - sig)) if code else torch.ones_like(Z)
+        want["pre"][r], tol["pre"][r] = y, steps_tol(K, mag) + half * y.abs()
+        want["out"][r] = (y * y_sig if code else y) + res[r].double()
+        tol["out"][r] = 1.13 * steps_tol(K, mag) + 2e-6 * (1 + y.abs()) + half * want["out"][r].abs()
+        if code:
+            want["dz"][r], tol["dz"][r] = G * slope, 4e-6 * G.abs() + half * (G * slope).abs()
+        want["da"][r], tol["da"][r] = G @ W, steps_tol(N, G.abs() @ W.abs()) + half * (G @ W).abs()
+        want["dw"][e], tol["dw"][e] = G.t() @ A, steps_tol(r.stop - r.start, G.abs().t() @ A.abs()) + 2 * ref.U24 * (G.t() @ A).abs()
+        want["db"][e], tol["db"][e] = (G * slope).sum(0), (2 * math.sqrt(R) * 1.13 * ref.U24 + 4e-6 * (code > 0)) * G.abs().sum(0)
+    for k, (buf, dtype) in dict(out=(out, BF), pre=(pre, BF), dz=(dz, BF), da=(da, BF), dw=(dw, torch.float32), db=(db, torch.float32)).items():
+        near(buf.view(dtype, *want[k].shape), want[k], tol[k], k)
 
 
 @pytest.mark.parametrize("name", BAD)
