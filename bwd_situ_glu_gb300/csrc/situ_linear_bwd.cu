@@ -23,20 +23,26 @@ using namespace situ_linear;
 
 // ---------------------------------------------------------------- dz and the bias gradient
 
-// Bias sums of 16384 rows x 3584: 28 us with the second kernel (117 MB; 17.5 us at the copy rate).
+// Bias sums of 16384 rows x 3584: 22 us with the second kernel (117 MB; 17.5 us at the copy rate).
 //
 // Rows are cut into pieces of piece_rows() rows of one expert; a block takes a piece's 256 columns at a time
 // (8 per lane, its warps take rows in turn), adds its warps' sums in order and leaves them in
-// part[piece][column]; the second kernel adds an expert's pieces in order. No result depends on timing.
+// part[piece][column]; the second kernel adds an expert's pieces, every SUM_CHAINS-th in a chain of its own and the chains
+// in order. No result depends on timing.
 constexpr int BIAS_WARPS = 8;
 constexpr int BIAS_COLS = 256;
-constexpr int MIN_PIECE = 16, MAX_PIECE = 128;
+constexpr int MIN_PIECE = 16, MAX_PIECE = 128, MANY_PIECES = 2048;
+constexpr int SUM_CHAINS = 8;
+constexpr int64_t SPLIT_PIECES = 16;         // pieces of an expert, on average, from which a chain is a warp's
 
 // 128 rows, or fewer (two a warp at least, 64 pieces of an expert at most) until there are some four blocks an SM:
-// 461 x 1088 through silu took 28.9 us with 128.
+// 461 x 1088 through silu took 28.9 us with 128. Above MANY_PIECES they grow with the root of the rows: a chain of fp32
+// additions is at most 2·sqrt(R) long (one of R/128 lost 0.4 % of the sum of 2^25 equal values), and
+// the walk over them is short (2^20 x 3584: 1.06 ms in all, 1.12 at the copy rate; pieces of 128 rows 2.24).
 int64_t piece_rows(int64_t R, int64_t N, int64_t E) {
     int64_t piece = MAX_PIECE;
     while (piece > MIN_PIECE && (R / piece + E) * ((N + BIAS_COLS - 1) / BIAS_COLS) < 600 && R / E / piece < 32) piece /= 2;
+    while (R / piece > MANY_PIECES && R / piece > piece) piece *= 2;
     return piece;
 }
 
@@ -114,11 +120,16 @@ __global__ void __launch_bounds__(BIAS_WARPS * 32)
     }
 }
 
-// blockIdx.y: expert; blockIdx.x: 256 columns.
+// blockIdx.y: expert; blockIdx.x: BIAS_COLS columns, their chains in a thread's registers, or 32 columns, a chain a
+// warp (SPLIT, for experts of many pieces: 16384 x 3584 for one weight, 128 pieces, 32.9 us in registers, 21.8 split; 256 experts
+// of 1024 x 1024, 8 pieces each, 87.5 and 100.6). The same sums either way.
+template <bool SPLIT>
 __global__ void __launch_bounds__(BIAS_COLS)
     bias_sum_kernel(const float* __restrict__ part, const int64_t* __restrict__ offsets, float* __restrict__ dbias,
                     int64_t R, int64_t N, int piece) {
-    const int e = blockIdx.y, lane = threadIdx.x & 31;
+    static_assert(SUM_CHAINS == BIAS_COLS / 32, "a chain a warp");
+    const int e = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float s_chain[SUM_CHAINS][32];
     __shared__ int s_first[BIAS_COLS / 32];
     __shared__ int s_count[MAX_EXPERTS];
     const bool orderly = each_expert(offsets, (int)gridDim.y, R, [&](int i, int64_t b, int64_t en) {
@@ -128,18 +139,36 @@ __global__ void __launch_bounds__(BIAS_COLS)
     int first = 0;                           // pieces of the experts before e
     for (int i = threadIdx.x; i < e; i += blockDim.x) first += s_count[i];
     first = (int)__reduce_add_sync(FULL_MASK, (unsigned)first);
-    if (lane == 0) s_first[threadIdx.x >> 5] = first;
+    if (lane == 0) s_first[warp] = first;
     __syncthreads();
     first = 0;
 #pragma unroll
     for (int i = 0; i < BIAS_COLS / 32; ++i) first += s_first[i];
     const int64_t n = s_count[e];
-    const int64_t c = (int64_t)blockIdx.x * BIAS_COLS + threadIdx.x;
-    if (c >= N) return;
-    float v = 0.0f;
+    const int64_t c = (int64_t)blockIdx.x * (SPLIT ? 32 : BIAS_COLS) + (SPLIT ? lane : threadIdx.x);
+    const float* at = part + first * N + c;
+    float v[SUM_CHAINS] = {};
+    if constexpr (SPLIT) {
+        if (c < N) {
 #pragma unroll 8
-    for (int64_t i = 0; i < n; ++i) v += part[(first + i) * N + c];
-    dbias[(int64_t)e * N + c] = v;
+            for (int64_t i = warp; i < n; i += SUM_CHAINS) v[0] += at[i * N];
+        }
+        s_chain[warp][lane] = v[0];
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int k = 0; k < SUM_CHAINS; ++k) v[k] = s_chain[k][lane];
+    } else if (c < N) {
+        for (int64_t i = 0; i < n; i += SUM_CHAINS) {
+#pragma unroll
+            for (int k = 0; k < SUM_CHAINS; ++k)
+                if (i + k < n) v[k] += at[(i + k) * N];
+        }
+    }
+    if (c >= N) return;
+#pragma unroll
+    for (int k = 1; k < SUM_CHAINS; ++k) v[0] += v[k];
+    dbias[(int64_t)e * N + c] = v[0];
 }
 
 // ---------------------------------------------------------------- the weight gradient
@@ -511,8 +540,11 @@ int situ_linear_act_bwd(const void* dout, const void* pre, int act, const int64_
         if (e != cudaSuccess) return cuda_fail(e);
     }
     if (dbias) {
-        bias_sum_kernel<<<dim3((unsigned)((N + BIAS_COLS - 1) / BIAS_COLS), (unsigned)E), BIAS_COLS, 0, stream>>>(
-            (const float*)workspace, expert_offsets, dbias, R, N, piece);
+        const bool split = R / piece / E >= SPLIT_PIECES;
+        const int64_t cols = split ? 32 : BIAS_COLS;
+        auto kernel = split ? bias_sum_kernel<true> : bias_sum_kernel<false>;
+        kernel<<<dim3((unsigned)((N + cols - 1) / cols), (unsigned)E), BIAS_COLS, 0, stream>>>((const float*)workspace,
+                                                                                              expert_offsets, dbias, R, N, piece);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e);
     }

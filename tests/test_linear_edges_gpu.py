@@ -66,3 +66,27 @@ def test_gelu_gradient_accuracy():
     cdf = 0.5 * torch.special.erfc(-z.double() / math.sqrt(2)).numpy()
     zphi = np.abs(zd) * np.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
     ref.near(db, ref.act(zd, "gelu")[1], gelu_rel(np.abs(zd)) * (cdf + zphi), "dbias")
+
+
+@pytest.mark.parametrize("R", [2 ** 25, 2 ** 25 - 77])
+def test_bias_gradient_of_many_rows(R):
+    """Equal values make roundings add up: 1 + 2^-7 summed over 2^25 rows in one chain of 128-row pieces loses 2^-8 of the
+    sum. Chains of at most 2·sqrt(R) additions stay within 2·sqrt(R)·2^-24."""
+    N = 8
+    dout = torch.full((R, N), 1 + 2.0 ** -7, dtype=BF, device=DEV)
+    _, _, db = sg.situ_linear_bwd(dout, None, torch.zeros(N, 8, dtype=BF, device=DEV), need_da=False, need_dw=False)
+    want = np.full(N, R * (1 + 2.0 ** -7))
+    ref.near(db, want, 2 * math.sqrt(R) * ref.U24 * want, "dbias")
+
+
+def test_bias_gradient_of_many_ragged_rows():
+    """Experts of 0 to 400000 rows, 1.1 million in all: pieces of more than 128 rows that end inside an expert."""
+    counts = [400_000, 0, 1, 299_999, 128, 400_001]
+    R, N = sum(counts), 40
+    g = torch.Generator(device=DEV).manual_seed(2)
+    dout = torch.randn(R, N, generator=g, device=DEV).to(BF)
+    off = torch.tensor([0, *np.cumsum(counts)], dtype=torch.int64, device=DEV)
+    _, _, db = sg.situ_linear_bwd(dout, None, torch.zeros(len(counts), N, 8, dtype=BF, device=DEV), off, need_da=False, need_dw=False)
+    for e in range(len(counts)):
+        x = dout[off[e]:off[e + 1]].double()
+        ref.near(db[e], x.sum(0).cpu().numpy(), (2 * math.sqrt(R) * ref.U24 * x.abs().sum(0)).cpu().numpy(), f"dbias {e}")
