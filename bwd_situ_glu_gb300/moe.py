@@ -400,8 +400,9 @@ def _autograd():
 
     class Linear(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, a, w, bias, residual, expert_offsets, act):
-            keep = act != "none" and any(ctx.needs_input_grad[:3])
+        def forward(ctx, a, w, bias, residual, expert_offsets, act, grad):
+            # needs_input_grad goes by the inputs alone; without grad mode there is no backward to keep anything for
+            keep = act != "none" and grad and any(ctx.needs_input_grad[:3])
             out = situ_linear(a, w, expert_offsets, bias, residual, act, save_pre=keep)
             out, pre = out if keep else (out, None)
             ctx.save_for_backward(a, w, expert_offsets, pre, bias if keep else None)
@@ -413,12 +414,12 @@ def _autograd():
             a, w, expert_offsets, pre, bias = ctx.saved_tensors
             need = ctx.needs_input_grad
             if not any(need[:3]):      # the residual's alone: no pre was kept
-                return None, None, None, dout, None, None
+                return None, None, None, dout, None, None, None
             dout = dout.contiguous()
             da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=_BF16,
                                          bias=need[2], need_da=need[0], need_dw=need[1])
             da, dw, db = once((da, dw, db), dout, a, w, bias)
-            return da, dw, db, dout if need[3] else None, None, None
+            return da, dw, db, dout if need[3] else None, None, None, None
 
     _functions = (RouteTopk, Dispatch, Combine, Linear)
     return _functions
@@ -442,4 +443,4 @@ def moe_combine(o, weights, row_of, expert_offsets, residual=None):
 def linear(a, w, bias=None, residual=None, expert_offsets=None, act="none"):
     """situ_linear (bf16 out), differentiable in a, w (gradient in bf16, as PyTorch's autograd wants),
     bias and residual. Gradients of rows that belong to no expert are undefined."""
-    return _autograd()[3].apply(a, w, bias, residual, expert_offsets, act)
+    return _autograd()[3].apply(a, w, bias, residual, expert_offsets, act, torch.is_grad_enabled())

@@ -4,6 +4,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import bwd_situ_glu_gb300 as sg
 
@@ -56,3 +57,57 @@ def test_star_import():
     names = {}
     exec("from bwd_situ_glu_gb300 import *", names)
     assert names["situ_linear"] is sg.situ_linear and names["moe"] is sg.moe and names["situ_glu_fwd"] is sg.situ_glu_fwd
+
+
+# ---------------------------------------------------------------- which kernels the autograd operators call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The kernels' bindings replaced by ones that note their call and return tensors of the right shape."""
+    made = []
+
+    def linear(a, w, expert_offsets=None, bias=None, residual=None, act="none", save_pre=False, **kw):
+        made.append(("linear", dict(save_pre=save_pre, **kw)))
+        out = torch.zeros(a.shape[0], w.shape[-2], dtype=torch.bfloat16)
+        return (out, out.clone()) if save_pre else out
+
+    def linear_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, dw_dtype=None, bias=True, need_da=True, need_dw=True, **kw):
+        made.append(("linear_bwd", dict(pre=pre is not None, bias=bias, need_da=need_da, need_dw=need_dw, **kw)))
+        return (torch.zeros_like(a) if need_da else None, torch.zeros_like(w) if need_dw else None,
+                torch.zeros(w.shape[:-1]) if bias else None)
+
+    def combine(o, row_of, weights=None, residual=None, **kw):
+        made.append(("combine", {}))
+        return torch.zeros(row_of.shape[0], o.shape[1], dtype=o.dtype)
+
+    def combine_bwd(dy, o, row_of, weights, expert_offsets, **kw):
+        made.append(("combine_bwd", {}))
+        return torch.zeros_like(o), torch.zeros(row_of.shape)
+
+    for name, f in dict(situ_linear=linear, situ_linear_bwd=linear_bwd, situ_combine=combine, situ_combine_bwd=combine_bwd).items():
+        monkeypatch.setattr(sg.moe, name, f)
+    return made
+
+
+def linear_inputs(*needed):
+    ts = [torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(8, 16, dtype=torch.bfloat16), torch.zeros(8),
+          torch.zeros(4, 8, dtype=torch.bfloat16)]
+    return [t.requires_grad_(i in needed) for i, t in enumerate(ts)]
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_linear_without_grad_keeps_nothing(calls, mode):
+    """Weights that require gradients, but no grad mode: the value before the activation is not written."""
+    ts = linear_inputs(1, 2)
+    with mode():
+        out = sg.moe.linear(*ts, act="silu")
+    assert not out.requires_grad and calls == [("linear", dict(save_pre=False))]
+
+
+def test_linear_with_grad_keeps_what_it_needs(calls):
+    for needed, act, pre in (((1,), "silu", True), ((3,), "silu", False), ((0, 1, 2), "none", False)):
+        calls.clear()
+        sg.moe.linear(*linear_inputs(*needed), act=act).sum().backward()
+        assert calls[0] == ("linear", dict(save_pre=pre))
+        assert [c[0] for c in calls[1:]] == (["linear_bwd"] if needed != (3,) else [])
