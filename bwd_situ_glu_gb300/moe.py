@@ -391,6 +391,8 @@ def _autograd():
         @staticmethod
         def backward(ctx, dy):
             o, weights, row_of, expert_offsets = ctx.saved_tensors
+            if not any(ctx.needs_input_grad[:2]):      # the residual's alone
+                return None, None, dy, None, None
             plain = weights is None    # a sum: the weights are ones without a gradient
             if plain:
                 weights = torch.ones(row_of.shape, dtype=_F32, device=o.device)

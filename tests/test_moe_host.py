@@ -111,3 +111,16 @@ def test_linear_with_grad_keeps_what_it_needs(calls):
         sg.moe.linear(*linear_inputs(*needed), act=act).sum().backward()
         assert calls[0] == ("linear", dict(save_pre=pre))
         assert [c[0] for c in calls[1:]] == (["linear_bwd"] if needed != (3,) else [])
+
+
+@pytest.mark.parametrize("needed,launches", [((2,), 0), ((0,), 1), ((1,), 1), ((0, 1, 2), 1)])
+def test_combine_backward_launches(calls, needed, launches):
+    """The residual's gradient is dy itself: no pass over the rows for it alone."""
+    o, w, res = (t.requires_grad_(i in needed) for i, t in enumerate((torch.zeros(8, 16), torch.zeros(4, 2), torch.zeros(4, 16))))
+    row_of, off = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)
+    dy = torch.rand(4, 16)
+    sg.moe.moe_combine(o, w, row_of, off, residual=res).backward(dy)
+    assert [c[0] for c in calls] == ["combine"] + ["combine_bwd"] * launches
+    assert [t.grad is not None for t in (o, w, res)] == [i in needed for i in range(3)]
+    if 2 in needed:
+        assert torch.equal(res.grad, dy)
