@@ -402,13 +402,13 @@ def _autograd():
 
     class Linear(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, a, w, bias, residual, expert_offsets, act, grad):
+        def forward(ctx, a, w, bias, residual, expert_offsets, act, status, grad):
             # needs_input_grad goes by the inputs alone; without grad mode there is no backward to keep anything for
             keep = act != "none" and grad and any(ctx.needs_input_grad[:3])
-            out = situ_linear(a, w, expert_offsets, bias, residual, act, save_pre=keep)
+            out = situ_linear(a, w, expert_offsets, bias, residual, act, save_pre=keep, status=status)
             out, pre = out if keep else (out, None)
             ctx.save_for_backward(a, w, expert_offsets, pre, bias if keep else None)
-            ctx.act = act
+            ctx.act, ctx.status = act, status   # not saved as a tensor: the kernels write it
             return out
 
         @staticmethod
@@ -416,12 +416,12 @@ def _autograd():
             a, w, expert_offsets, pre, bias = ctx.saved_tensors
             need = ctx.needs_input_grad
             if not any(need[:3]):      # the residual's alone: no pre was kept
-                return None, None, None, dout, None, None, None
+                return None, None, None, dout, None, None, None, None
             dout = dout.contiguous()
             da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=_BF16,
-                                         bias=need[2], need_da=need[0], need_dw=need[1])
+                                         bias=need[2], need_da=need[0], need_dw=need[1], status=ctx.status)
             da, dw, db = once((da, dw, db), dout, a, w, bias)
-            return da, dw, db, dout if need[3] else None, None, None, None
+            return da, dw, db, dout if need[3] else None, None, None, None, None
 
     _functions = (RouteTopk, Dispatch, Combine, Linear)
     return _functions
@@ -442,7 +442,8 @@ def moe_combine(o, weights, row_of, expert_offsets, residual=None):
     return _autograd()[2].apply(o, weights, residual, row_of, expert_offsets)
 
 
-def linear(a, w, bias=None, residual=None, expert_offsets=None, act="none"):
+def linear(a, w, bias=None, residual=None, expert_offsets=None, act="none", status=None):
     """situ_linear (bf16 out), differentiable in a, w (gradient in bf16, as PyTorch's autograd wants),
-    bias and residual. Gradients of rows that belong to no expert are undefined."""
-    return _autograd()[3].apply(a, w, bias, residual, expert_offsets, act, torch.is_grad_enabled())
+    bias and residual. Gradients of rows that belong to no expert are undefined. ``status`` as in
+    situ_linear, for the backward's kernels too."""
+    return _autograd()[3].apply(a, w, bias, residual, expert_offsets, act, status, torch.is_grad_enabled())

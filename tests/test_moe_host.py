@@ -102,14 +102,14 @@ def test_linear_without_grad_keeps_nothing(calls, mode):
     ts = linear_inputs(1, 2)
     with mode():
         out = sg.moe.linear(*ts, act="silu")
-    assert not out.requires_grad and calls == [("linear", dict(save_pre=False))]
+    assert not out.requires_grad and len(calls) == 1 and calls[0][1]["save_pre"] is False
 
 
 def test_linear_with_grad_keeps_what_it_needs(calls):
     for needed, act, pre in (((1,), "silu", True), ((3,), "silu", False), ((0, 1, 2), "none", False)):
         calls.clear()
         sg.moe.linear(*linear_inputs(*needed), act=act).sum().backward()
-        assert calls[0] == ("linear", dict(save_pre=pre))
+        assert calls[0][0] == "linear" and calls[0][1]["save_pre"] is pre
         assert [c[0] for c in calls[1:]] == (["linear_bwd"] if needed != (3,) else [])
 
 
@@ -124,3 +124,10 @@ def test_combine_backward_launches(calls, needed, launches):
     assert [t.grad is not None for t in (o, w, res)] == [i in needed for i in range(3)]
     if 2 in needed:
         assert torch.equal(res.grad, dy)
+
+
+def test_linear_status_reaches_every_kernel(calls):
+    """A timed-out wait is reported through the status word, in the forward and in the backward."""
+    status = torch.zeros(1, dtype=torch.int32)
+    sg.moe.linear(*linear_inputs(0, 1, 2, 3), act="gelu", status=status).sum().backward()
+    assert [c[0] for c in calls] == ["linear", "linear_bwd"] and all(c[1]["status"] is status for c in calls)
