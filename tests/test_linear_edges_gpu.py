@@ -90,3 +90,49 @@ def test_bias_gradient_of_many_ragged_rows():
     for e in range(len(counts)):
         x = dout[off[e]:off[e + 1]].double()
         ref.near(db[e], x.sum(0).cpu().numpy(), (2 * math.sqrt(R) * ref.U24 * x.abs().sum(0)).cpu().numpy(), f"dbias {e}")
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("counts", [[5, 0, 11], [140, 3, 130]], ids=str)
+@pytest.mark.parametrize("of", ["a", "w"])
+def test_gradient_by_differences_along_its_signs(counts, act, of):
+    """Central differences of <out, dout> (fp32 out) along the signs of the float64 gradient, where its entries add up to
+    some thirty times the tolerance: a gradient without act', or a zero one, does not pass.
+
+    d = dz/d(step). Differences: third derivative below 2, times d^3 eps^2 / 6, and the rounding of out over eps. Gradient:
+    act' off by act'' (below 1.2) times half an ulp of pre, dz by half an ulp, da by half an ulp."""
+    R, N, K, E = sum(counts), 40, 24, 3
+    g = torch.Generator().manual_seed(12)
+    a = (torch.randint(-8, 9, (R, K), generator=g) / 8).to(BF)
+    w = (torch.randint(-8, 9, (E, N, K), generator=g) / 32).to(BF)
+    bias, dout = torch.randn(E, N, generator=g) * 0.1, torch.randn(R, N, generator=g).to(BF)
+    offs = np.array([0, *np.cumsum(counts)])
+    off = torch.from_numpy(offs).to(DEV)
+    A, W, B, G = np64(a), np64(w), np64(bias), np64(dout)
+    _, z, smag = ref.linear(A, W, offs, B, None, "none")
+    want, flat = (ref.linear_bwd(G, A, W, offs, z, name)["d" + of] for name in (act, "none"))
+    v = np.where(want < 0, -1.0, 1.0)
+    eps = 2.0 ** -5 if of == "a" else 2.0 ** -6         # a ± eps and w ± eps are bf16 values
+    step = torch.from_numpy(v * eps)
+    _, pre = sg.situ_linear(a.to(DEV), w.to(DEV), off, bias=bias.to(DEV), act=act, save_pre=True)
+    da, dw, _ = sg.situ_linear_bwd(dout.to(DEV), a.to(DEV), w.to(DEV), off, act=act, pre=pre)
+
+    def loss(sign):
+        x, y = (a.double() + sign * step, w) if of == "a" else (a, w.double() + sign * step)
+        out = sg.situ_linear(x.to(BF).to(DEV), y.to(BF).to(DEV), off, bias=bias.to(DEV), act=act, out_dtype=torch.float32)
+        return (np64(out) * G).sum()
+
+    num = (loss(1) - loss(-1)) / (2 * eps)
+    d = np.abs(ref.linear(v, W, offs, None, None, "none")[0] if of == "a" else ref.linear(A, v, offs, None, None, "none")[0])
+    dabs, az = np.abs(G), np.abs(z)
+    tol = (dabs * (((K / 16 + 2) * 2.0 ** -22 * smag * 1.13 + 2e-6 * (1 + az)) / eps)).sum()
+    tol += (np.abs(want) * ref.BF16_HALF).sum() if of == "a" else 1e-5 * (dabs * d).sum()
+    if act != "none":
+        tol += (dabs * (d ** 3 * eps ** 2 / 3 + d * (1.2 * ref.BF16_HALF * az + 1.13 * ref.BF16_HALF + 4e-6))).sum()
+        assert abs((flat * v).sum() - num) > 10 * tol
+    assert tol < 0.05 * abs(num)
+    assert abs(num - (np64(da if of == "a" else dw) * v).sum()) <= tol
