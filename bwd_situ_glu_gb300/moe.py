@@ -152,8 +152,10 @@ def situ_dispatch_plan(ids, num_experts, p=None, stream=None):
 
 
 def situ_dispatch(x, row_of, expert_offsets, weights=None, h=None, stream=None):
-    """h [T*k, D]: h[row_of[t,j]] = x[t], or weights[t,j]*x[t] with weights fp32 [T,k]; rows that belong to no
-    token are zero. x [T,D] bf16 or fp32."""
+    """h [T*k, D]: h[row_of[t,j]] = x[t], or weights[t,j]*x[t] with weights fp32 [T,k]; rows from
+    expert_offsets[-1] on are zero. x [T,D] bf16 or fp32. row_of and expert_offsets are one plan's: a row before
+    expert_offsets[-1] that row_of does not name is not written, so a token-expert pair is dropped by its id
+    (-1) before the plan, not by its row_of after it."""
     ty = _type(x, "x")
     (T, D), k = _two(x, "x"), _two(row_of, "row_of")[1]
     dev = x.device
@@ -192,8 +194,9 @@ def situ_combine(o, row_of, weights=None, residual=None, y=None, stream=None):
 
 
 def situ_combine_bwd(dy, o, row_of, weights, expert_offsets, do=None, dweights=None, stream=None):
-    """(do [R,D] of o's type, dweights fp32 [T,k]): do[row_of[t,j]] = weights[t,j]*dy[t] (rows of no token are
-    zero), dweights[t,j] = <dy[t], o[row_of[t,j]]> (0 without a row)."""
+    """(do [R,D] of o's type, dweights fp32 [T,k]): do[row_of[t,j]] = weights[t,j]*dy[t] (rows from
+    expert_offsets[-1] on are zero; one before it that row_of does not name is not written, as in
+    situ_dispatch), dweights[t,j] = <dy[t], o[row_of[t,j]]> (0 without a row)."""
     ty = _type(o, "o")
     (R, D), (T, k) = _two(o, "o"), _two(row_of, "row_of")
     dev = o.device
@@ -433,12 +436,13 @@ def route_topk(logits, k):
 
 
 def moe_dispatch(x, row_of, expert_offsets):
-    """situ_dispatch, differentiable in x."""
+    """situ_dispatch, differentiable in x (row_of and expert_offsets of one plan, as there)."""
     return _autograd()[1].apply(x, row_of, expert_offsets)
 
 
 def moe_combine(o, weights, row_of, expert_offsets, residual=None):
-    """situ_combine, differentiable in o, weights (None: all 1) and residual."""
+    """situ_combine, differentiable in o, weights (None: all 1) and residual; row_of and expert_offsets are one
+    plan's (the gradient of o at a row before expert_offsets[-1] that row_of does not name is undefined)."""
     return _autograd()[2].apply(o, weights, residual, row_of, expert_offsets)
 
 

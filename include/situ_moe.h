@@ -69,8 +69,10 @@ int situ_dispatch_plan(const int32_t* ids, const float* p, int64_t* expert_offse
 
 /* h [R, D] of `type`: h[row_of[t, k]] = x[t] (weights NULL) or weights[t, k]·x[t] (weights fp32
  * [T, K]; the product in fp32, rounded once); rows from expert_offsets[E] on are zeroed. x [T, D]
- * of `type`; row_of entries outside [0, R) are skipped. Its gradient is situ_combine. Any D >= 1
- * (16-byte vectors where D and the pointers allow). */
+ * of `type`; row_of entries outside [0, R) are skipped. row_of and expert_offsets are those of one
+ * plan: a row before expert_offsets[E] that row_of does not name is not written (to drop a pair, give
+ * it no expert before the plan). Its gradient is situ_combine. Any D >= 1 (16-byte vectors where D and
+ * the pointers allow). */
 int situ_dispatch(const void* x, int type, const int32_t* row_of, const int64_t* expert_offsets, int64_t E,
                   const float* weights, void* h, int64_t T, int64_t K, int64_t R, int64_t D, cudaStream_t stream);
 
@@ -81,8 +83,8 @@ int situ_combine(const void* o, int type, const int32_t* row_of, const float* we
                  int64_t T, int64_t K, int64_t R, int64_t D, cudaStream_t stream);
 
 /* Its gradient: dout_rows [R, D] of `type`, row_of[t, k] = weights[t, k]·dy[t] (rounded once; rows
- * from expert_offsets[E] on are zeroed), and dweights fp32 [T, K] = <dy[t], o[row_of[t, k]]> (0
- * without a row). The residual's gradient is dy itself. */
+ * from expert_offsets[E] on are zeroed, others that row_of does not name are not written), and
+ * dweights fp32 [T, K] = <dy[t], o[row_of[t, k]]> (0 without a row). The residual's gradient is dy itself. */
 int situ_combine_bwd(const void* dy, const void* o, int type, const int32_t* row_of, const float* weights,
                      const int64_t* expert_offsets, int64_t E, void* dout_rows, float* dweights, int64_t T, int64_t K,
                      int64_t R, int64_t D, cudaStream_t stream);
@@ -93,13 +95,17 @@ int situ_combine_bwd(const void* dy, const void* o, int type, const int32_t* row
  * layout), bias fp32 [E, N] or NULL, residual bf16 [R, N] or NULL, out [R, N] of out_type, pre bf16
  * [R, N] or NULL (receives z rounded to bf16, what the backward reads). expert_offsets int64 [E+1],
  * or NULL with E = 1: one weight for all rows. Rows outside every expert's range are not written.
- * N % 8 == 0, K % 8 == 0; 1 <= E <= 1024; R <= 2^31 - 1025; a, w, residual, out and pre 16-byte aligned. status
- * (device int, zeroed by the caller, may be NULL) turns 1 if a pipeline wait timed out. */
+ * N % 8 == 0, K % 8 == 0; 1 <= E <= 1024; R <= 2^31 - 1025; a, w, residual, out and pre 16-byte
+ * aligned. status (device int, zeroed by the caller, may be NULL) turns 1 if a pipeline wait timed out.
+ * The tensor cores cut each 16-deep step's fp32 sum towards zero: an fp32 out is off by 1e-6 of its
+ * norm at K = 1024 and by 1.9e-5 at 16384 (situ_linear_wgrad, whose contraction is the rows, adds
+ * 512-row chunks rounded to nearest instead: 5e-7 at any R). */
 int situ_linear_fwd(const void* a, const void* w, const int64_t* expert_offsets, int64_t E, const float* bias,
                     const void* residual, int act, void* out, int out_type, void* pre, int* status, int64_t R,
                     int64_t N, int64_t K, cudaStream_t stream);
 
-/* dz = dout·act'(pre), rounded to bf16 (the operand of the two products below), and dbias fp32
+/* dz = dout·act'(pre), rounded to bf16 (the operand of the two products below, as a bf16 layer's
+ * gradients are: relative 1.7e-3 of the norm, in an fp32 dw too), and dbias fp32
  * [E, N] = the sum of the unrounded dz over each expert's rows. dout, pre and dz bf16 [R, N]; with
  * SITU_ACT_NONE pre and dz are not used (dz = dout) and may be NULL. dbias may be NULL; with it,
  * workspace holds situ_linear_act_bwd_workspace(R, N, E) bytes, 4-byte aligned. dz of rows outside

@@ -184,3 +184,35 @@ def test_fused_products_stay_bounded(call):
     t = ms(orderly), ms(overlapping)
     assert st.item() == 0
     assert t[1] < 5 * t[0], t
+
+
+def test_rows_without_a_token():
+    """Rows past the plan's last are zeroed; one before it that row_of does not name (a pair dropped after the plan) is not
+    written; dropped by its id before the plan, the pair has no row at all."""
+    T, K, D = 6, 2, 40
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x, w = torch.randn(T, D, generator=g, device=DEV), torch.rand(T, K, generator=g, device=DEV)
+    ids = torch.tensor([[0, 2], [1, -1], [2, 0], [0, 1], [-1, -1], [1, 2]], dtype=torch.int32, device=DEV)
+    offsets, row_of, _, _ = sg.situ_dispatch_plan(ids, 3)
+    n, R = int(offsets[-1]), T * K
+    assert n == 9
+    lost = int(row_of[3, 0])
+    dropped = row_of.clone()
+    dropped[3, 0] = -1
+    h, do = Guarded(R * D * 4), Guarded(R * D * 4)
+    hv, dv = h.view(torch.float32, R, D), do.view(torch.float32, R, D)
+    hv.fill_(7.0)
+    dv.fill_(7.0)
+    sg.situ_dispatch(x, dropped, offsets, h=hv)
+    sg.situ_combine_bwd(x, torch.ones(R, D, device=DEV), dropped, w, offsets, do=dv)
+    for buf in (hv, dv):
+        assert (buf[n:] == 0).all() and (buf[lost] == 7.0).all()
+    for t in range(T):
+        for k in range(K):
+            if dropped[t, k] >= 0:
+                assert torch.equal(hv[dropped[t, k]], x[t]) and torch.equal(dv[dropped[t, k]], w[t, k] * x[t])
+    ids[3, 0] = -1
+    offsets, row_of, _, _ = sg.situ_dispatch_plan(ids, 3)
+    hv.fill_(7.0)
+    sg.situ_dispatch(x, row_of, offsets, h=hv)
+    assert int(offsets[-1]) == n - 1 and (hv[n - 1:] == 0).all() and not (hv == 7.0).any()
