@@ -20,7 +20,8 @@ import bwd_situ_glu_gb300 as _sg
 from bwd_situ_glu_gb300 import _check, load as _lib
 
 # A decoding step's kernels take 3 to 5 us, an allocation and a launch through ctypes 5 us of host time; hence the
-# names bound here, the one expression per tensor in _need, and the raw stream handle (14.5 -> 9 us a call).
+# names bound here, the one expression per tensor in _need, and the raw stream handle: a third less host time a call (with
+# its allocations a one-kernel call takes 10.5 to 15 us, depending on the host).
 _T, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64
 _CODE = {_BF16: 0, _F32: 1}  # SITU_BF16, SITU_FP32
 _empty = torch.empty
