@@ -20,8 +20,9 @@ Binding names match the C entry points:
   streamed form moving gradients and weights chunk by chunk
 * ``situ_route_topk``, ``situ_dispatch_plan``, ``situ_dispatch``, ``situ_combine``, ``situ_linear`` and their
   gradients: the rest of the MoE layer (module ``moe``; C ABI ``include/situ_moe.h``)
-* ``situ_quant_fp8`` / ``situ_dequant_fp8``: E4M3 codes with power-of-two scales of 128-element blocks, the
-  operands of products in 8 bits (module ``fp8``; C ABI ``include/situ_fp8.h``)
+* ``situ_quant_fp8`` / ``situ_dequant_fp8``: E4M3 codes with power-of-two scales of 128-element blocks, and
+  ``situ_linear_fp8`` / ``situ_linear_fp8_bwd``: the products of such rows and weights (module ``fp8``; C ABI
+  ``include/situ_fp8.h``)
 * ``situ_and_mul(x, beta, linear_beta)``: autograd function (forward kernel; backward kernel
   with p = 1), the pages' operator interface
 
@@ -45,11 +46,12 @@ LIB_DIR = os.path.join(_HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libsitu_glu.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("situ_glu.cu", "situ_glu_fp8.cu", "situ_glu_dgrad.cu",
                                              "situ_glu_gateup.cu", "situ_adam.cu", "situ_glu_selftest.cu", "situ_route.cu",
-                                             "situ_dispatch.cu", "situ_linear.cu", "situ_linear_bwd.cu", "situ_quant.cu")]
+                                             "situ_dispatch.cu", "situ_linear.cu", "situ_linear_bwd.cu", "situ_quant.cu",
+                                             "situ_linear_fp8.cu")]
 # per-source extra flags: the host Adam update is a fixed sequence of IEEE fp32 operations
 SOURCE_FLAGS = {"situ_adam.cu": ["-Xcompiler", "-ffp-contract=off,-fno-fast-math,-fno-math-errno"]}
 DEPENDS = SOURCES + [os.path.join(CSRC, n) for n in ("situ_math.cuh", "situ_device.cuh", "situ_host.h",
-                                                     "situ_tc.cuh", "situ_pair.cuh", "situ_linear.cuh", "situ_fp8.cuh")] + [
+                                                     "situ_tc.cuh", "situ_pair.cuh", "situ_linear.cuh", "situ_linear_tc.cuh", "situ_fp8.cuh")] + [
     os.path.join(INCLUDE, n) for n in ("situ_glu.h", "situ_moe.h", "situ_fp8.h")]
 
 NVCC_FLAGS = [
@@ -176,6 +178,8 @@ def _declare_moe(lib):
             ("situ_linear_wgrad_workspace", [i64, i64, i64, i64], i64),
             ("situ_quant_fp8", [vp, cint, vp, vp, i64, i64, i64, cint, vp], cint),
             ("situ_dequant_fp8", [vp, vp, vp, cint, i64, i64, i64, cint, vp], cint),
+            ("situ_linear_fp8_fwd", [vp, vp, vp, vp, vp, i64, vp, vp, cint, vp, cint, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_linear_fp8_dgrad", [vp, vp, vp, vp, vp, i64, vp, vp, i64, i64, i64, vp], cint),
             ("situ_linear_selftest_wait_timeout", [vp, vp, vp], cint),
             ("situ_linear_wgrad", [vp, vp, vp, i64, vp, cint, vp, i64, vp, i64, i64, i64, vp], cint)):
         fn = getattr(lib, name)
@@ -539,7 +543,7 @@ def situ_adam_stream_step(grad, weight, master, m, v, params: AdamParams, stagin
 
 _MOE_NAMES = ("situ_route_topk", "situ_route_topk_bwd", "situ_dispatch_plan", "situ_dispatch", "situ_combine",
               "situ_combine_bwd", "situ_linear", "situ_linear_bwd")
-_FP8_NAMES = ("situ_quant_fp8", "situ_dequant_fp8")
+_FP8_NAMES = ("situ_quant_fp8", "situ_dequant_fp8", "situ_linear_fp8", "situ_linear_fp8_bwd")
 _MODULES = {"moe": _MOE_NAMES, "fp8": _FP8_NAMES}
 
 

@@ -1,0 +1,552 @@
+// situ_linear_fp8.cu — matrix product of quantised rows with their expert's (or the one dense) quantised weight, with bias,
+// activation and residual in the epilogue, and the input gradient (include/situ_fp8.h).
+//
+//   forward   out[r] = act(Σ_kb 2^(ea[r,kb] + ew[·,kb]) Σ_{k in kb} a[r,k]·W_e[·,k] + b_e) + residual[r]
+//   dgrad     da[r]  = the same over blocks of dz[r] and W_eᵀ
+//
+// As the bf16 product (situ_linear.cu): pairs of SMs, the weights as the MMA's 256-row operand, the rows as its N operand.
+// What differs:
+//   * tcgen05.mma kind::mxf8f6f4 with block scales: the tensor core multiplies each 32-deep step of a row by a
+//     power of two held as a byte in TMEM, so the scales of 128-deep blocks cost neither instructions in the epilogue
+//     nor a rounding. A fifth role, the scale warp of each CTA, writes the bytes of a ring stage (its 128 weight
+//     rows': one byte for all; the chunk's rows': one each) in the layout that tcgen05.cp takes; the MMA warp copies them to
+//     TMEM in front of the stage's four MMAs. Each byte stands four times in a word, once for each MMA of the block.
+//   * two accumulators and the scales share TMEM's 512 columns, so a chunk has at most 224 rows.
+//   * the dgrad reads W_e as stored (contraction apart, "MN-major"): boxes of 128 columns x 128 rows of bytes.
+//   * linear_fp8_few_kernel: for few rows per expert, as there.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/situ_fp8.h"
+#include "situ_device.cuh"
+#include "situ_fp8.cuh"
+#include "situ_host.h"
+#include "situ_linear.cuh"
+#include "situ_linear_tc.cuh"
+#include "situ_pair.cuh"
+
+namespace {
+
+using namespace situ;
+using namespace situ_host;
+using namespace situ_pair;
+using namespace situ_linear;
+using namespace situ_linear_tc;
+using namespace situ_fp8;
+
+constexpr int KB8 = 128;                     // elements (bytes) of the contraction per ring stage: one scale block
+constexpr int UK8 = 32;                      // elements per tcgen05.mma
+constexpr int MAX_CHUNK = 224;               // rows per job
+constexpr int ACC_COLS = 224;                // TMEM columns of an accumulator
+constexpr int SCALE_WARP = 2 + NUM_EPI_WARPS;
+constexpr int NUM_THREADS = (SCALE_WARP + 1) * 32;    // TMA, MMA, epilogue, scales
+
+// Scale bytes of a stage in shared memory: 128 rows are 512 bytes, row i at 16·(i % 32) + 4·(i / 32), as tcgen05.cp
+// 32x128b takes them. One such piece for the weights, two for the rows.
+constexpr int SCALE_PIECE = 512;
+constexpr int SCALE_BYTES = 3 * SCALE_PIECE;
+constexpr int SCALE_COL0 = 2 * ACC_COLS;     // in TMEM: 4 columns a piece
+constexpr int SCALE_SLOTS = 5;               // stages whose scales TMEM holds; the tensor core takes copies and MMAs in order
+static_assert(SCALE_COL0 + SCALE_SLOTS * 12 <= TMEM_COLS, "TMEM columns");
+
+// A ring stage: 128 weight rows and half of the chunk's rows, 128 bytes each.
+__host__ __device__ constexpr int stage_bytes(int most) { return PA_BYTES + most / 2 * KB8; }
+constexpr int RING_BYTES = 6 * stage_bytes(MAX_CHUNK);
+__host__ __device__ constexpr int ring_stages(int most) {
+    const int s = RING_BYTES / stage_bytes(most);
+    return s < PSTAGES ? s : PSTAGES;
+}
+
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + PSTAGES * SCALE_BYTES + NUM_EPI_WARPS * PATCH + (int)sizeof(PairBars) + (int)sizeof(Plan);
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+
+// Instruction descriptor, kind::mxf8f6f4 on a pair: fp32 accumulate, E4M3 operands (formats 0), E8M0 scales (bit 23), scale
+// bytes 0 of their words, M = 256, N columns (a multiple of 32); bit 15: A stored MN-major.
+__device__ __forceinline__ uint32_t scaled_idesc(int n, bool a_mn) {
+    return ((uint32_t)a_mn << 15) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(256 >> 7) << 27);
+}
+
+__device__ __forceinline__ void scaled_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa_tmem,
+                                           uint32_t sb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Shared-memory descriptor of a piece of scales: no swizzle, 8 rows of 16 bytes are 128 bytes on.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// A piece to four TMEM columns of all four lane quadrants, in both CTAs (each from its own shared memory).
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// An MN-major tile of 128 columns (bytes) x 128 deep, as a TMA box writes it: a row of the contraction is 128 bytes, eight
+// are a 1024-byte swizzle atom (stride byte offset); there is no second 128 columns (leading byte offset unused).
+// The same fields as a K-major tile's.
+__device__ __forceinline__ uint64_t smem_desc_mn8(uint32_t saddr) { return smem_desc(saddr); }
+
+struct RowMaps {
+    CUtensorMap m[4];                        // boxes of 128 >> i rows
+};
+
+// Where a weight's scale bytes are: expert e's block of output columns c and block kb of the contraction at
+// e·per_expert + c·col_step + kb·k_step.
+struct ScaleStrides {
+    int64_t per_expert;
+    int col_step, k_step, col_blocks;
+};
+
+template <bool W_MN, int ACT>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    linear_fp8_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_r,
+                         const uint8_t* __restrict__ row_scales, const uint8_t* __restrict__ w_scales, ScaleStrides ws,
+                         const int64_t* __restrict__ offsets, const float* __restrict__ bias,
+                         const uint16_t* __restrict__ residual, void* __restrict__ out, int out_fp32,
+                         uint16_t* __restrict__ pre, int* __restrict__ status, int E, int64_t R, int64_t NCOL, int KB,
+                         int most) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* scales = ring + RING_BYTES;
+    uint8_t* patches = scales + PSTAGES * SCALE_BYTES;
+    PairBars* bars = (PairBars*)(patches + NUM_EPI_WARPS * PATCH);
+    Plan& plan = *(Plan*)(bars + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int NT = (int)((NCOL + TILE - 1) / TILE);
+    const int sbytes = stage_bytes(most), stages = ring_stages(most);
+
+    build_plan(plan, offsets, E, R, most);
+    // a full stage: the loads' bytes, announced by the leader's producer, and both CTAs' scales
+    const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS, 3);
+    const int jobs = plan.start[E] * NT;
+    const int j0 = blockIdx.x >> 1, jstep = gridDim.x >> 1;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs; the warp converged, one lane issues)
+        const bool elected = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, pending = 0, pend_par = 0;
+        const uint64_t pol_w = make_policy<kHintB>(), pol_r = make_policy<kHintA>();
+        bool ok = true;
+        Job next = {};
+        if (j0 < jobs) next = job_at(j0, plan, E, NT);
+        for (int j = j0; ok && j < jobs; j += jstep) {
+            const Job q = next;
+            const int c0 = q.nt * TILE + rank * 128;
+            const uint32_t bytes = (uint32_t)(2 * PA_BYTES + q.n * KB8);
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!pair_wait(&bars->empty[stage], phase ^ 1, &bars->abort, status)) { ok = false; break; }
+                if (elected) {
+                    if (rank == 0) mbar_expect_tx(&bars->full[stage], bytes);
+                    const uint32_t bar = cluster_addr(&bars->full[stage], 0);
+                    uint8_t* sa = ring + stage * sbytes;
+                    if constexpr (W_MN) pair_load_3d(sa, &map_w, c0, kb * KB8, q.e, bar, pol_w);
+                    else pair_load_3d(sa, &map_w, kb * KB8, c0, q.e, bar, pol_w);
+                    const int half = q.n >> 1;                   // rows of this CTA: a multiple of 16
+                    int at = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (half & (128 >> i)) {
+                            pair_load_2d(sa + PA_BYTES + at * KB8, &map_r.m[i], kb * KB8, q.row0 + rank * half + at, bar, pol_r);
+                            at += 128 >> i;
+                        }
+                    }
+                }
+                pending |= 1u << stage;
+                pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == stages) { stage = 0; phase ^= 1; }
+                if (kb == 0 && j + jstep < jobs) next = job_at(j + jstep, plan, E, NT);   // while these loads fly
+            }
+        }
+        __syncwarp();
+        if (rank == 0) pair_drain(bars, pending, pend_par);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader; the warp converged, one lane issues)
+        if (rank == 0) {
+            const bool elected = elect_one();
+            int stage = 0, job = 0, slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            int n_next = j0 < jobs ? job_at(j0, plan, E, NT).n : 0;
+            const uint32_t ring_addr = smem_addr(ring), scale_addr = smem_addr(scales);
+            for (int j = j0; ok && j < jobs; j += jstep, ++job) {
+                const int n = n_next;
+                const uint32_t idesc = scaled_idesc(n, W_MN);
+                const int acc = job & 1;
+                const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
+                if (!pair_wait<true>(&bars->tempty[acc], (uint32_t)((job >> 1) & 1) ^ 1, &bars->abort, status)) break;
+                tc_fence_after();
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!pair_wait<true>(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sa = ring_addr + (uint32_t)(stage * sbytes);
+                    const uint64_t ad = W_MN ? smem_desc_mn8(sa) : smem_desc(sa), bd = smem_desc(sa + PA_BYTES);
+                    const uint64_t sd = scale_desc(scale_addr + (uint32_t)(stage * SCALE_BYTES));
+                    const uint32_t sft = tmem + (uint32_t)(SCALE_COL0 + slot * 12);
+                    if (elected) {
+                        copy_scales(sft, sd);
+                        copy_scales(sft + 4, sd + (SCALE_PIECE >> 4));
+                        if (n > 128) copy_scales(sft + 8, sd + 2 * (SCALE_PIECE >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < KB8 / UK8; ++kk)   // 32 deep: 32 bytes along a row, 4096 bytes MN-major
+                            scaled_mma(d, ad + (uint64_t)(kk * (W_MN ? 256 : 2)), bd + (uint64_t)(kk * 2), idesc, sft, sft + 4,
+                                       kk > 0 ? 1u : (uint32_t)kb);
+                        pair_commit(&bars->empty[stage]);
+                    }
+                    if (++stage == stages) { stage = 0; phase ^= 1; }
+                    if (++slot == SCALE_SLOTS) slot = 0;
+                    if (kb == 0 && j + jstep < jobs) n_next = job_at(j + jstep, plan, E, NT).n;   // while these run
+                }
+                if (ok && elected) pair_commit(&bars->tfull[acc]);
+            }
+            __syncwarp();
+            if (elected) pair_commit(&bars->mma_done);
+        }
+    } else if (warp == SCALE_WARP) {
+        // ------------------------------------------------ scales (both CTAs): lane l has rows l, l + 32, .. of the chunk
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int j = j0; ok && j < jobs; j += jstep) {
+            const Job q = job_at(j, plan, E, NT);
+            const int cb = q.nt * 2 + rank;                      // this CTA's block of output columns
+            const uint8_t* wp = w_scales + q.e * ws.per_expert + (int64_t)cb * ws.col_step;
+            const uint8_t* rp = row_scales + (int64_t)(q.row0 + lane) * KB;
+            uint32_t b[8];
+            uint32_t wb;
+            auto fetch = [&](int kb) {
+                wb = cb < ws.col_blocks ? __ldg(wp + (int64_t)kb * ws.k_step) : 127u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b[i] = lane + 32 * i < q.rows ? __ldg(rp + (int64_t)(32 * i) * KB + kb) : 127u;
+            };
+            fetch(0);
+            for (int kb = 0; kb < KB; ++kb) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = b[i] * 0x01010101u;
+                const uint32_t w = wb * 0x01010101u;
+                if (kb + 1 < KB) fetch(kb + 1);
+                if (!pair_wait(&bars->empty[stage], phase ^ 1, &bars->abort, status)) { ok = false; break; }
+                uint8_t* at = scales + stage * SCALE_BYTES + lane * 16;
+                st_shared_v4(at, w, w, w, w);
+                st_shared_v4(at + SCALE_PIECE, v[0], v[1], v[2], v[3]);
+                st_shared_v4(at + 2 * SCALE_PIECE, v[4], v[5], v[6], v[7]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars->full[stage], 0));
+                if (++stage == stages) { stage = 0; phase ^= 1; }
+            }
+        }
+    } else {
+        linear_epilogue<ACT>(bars, plan, tmem, ACC_COLS, patches, bias, residual, out, out_fp32, pre, status, E, NCOL, NT, j0,
+                             jstep, jobs, rank);
+    }
+    pair_teardown(tmem, bars);
+}
+
+// ---------------------------------------------------------------- few rows per expert
+
+// A decoding step: the read of the weights is the whole cost. As linear_few_kernel: a job is 16 weight rows and up to
+// FEW_ROWS rows of one expert, the warps of a block share the contraction in steps of 256 (two scale blocks), and
+// the products run on mma.m16n8k16 with the codes as fp16, which holds every E4M3 number. A lane's 16-byte
+// loads of weights and of the row at the same place are the fragments of four steps, the contraction's order being
+// free within a block. A block's sum is multiplied by its scales as it is added to the fp32 total.
+constexpr int FEW_WARPS = 8;
+constexpr int FEW_ROWS = 32;                 // rows of one job: 1, 2 or 4 tiles of 8
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes as fp16.
+__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+    return h;
+}
+
+// x·2^(ea + ew - 254): in two factors, since their product may leave fp32 where the result does not.
+__device__ __forceinline__ float2 scale_factors(uint32_t ea, uint32_t ew) {
+    const int e = (int)(ea + ew) - 254;
+    const int first = max(-126, min(127, e)), second = max(-126, min(127, e - first));
+    float2 f = make_float2(__uint_as_float((uint32_t)(first + 127) << 23), __uint_as_float((uint32_t)(second + 127) << 23));
+    if (ea == 255 || ew == 255) f.x = __uint_as_float(0x7FFFFFFFu);
+    return f;
+}
+
+struct FewShared {
+    float part[FEW_WARPS][FEW_ROWS][17];     // [warp][row][weight row], padded
+};
+
+template <int NTT>
+__device__ __forceinline__ void few_job(FewShared& sh, const uint8_t* a, const uint8_t* as, const uint8_t* we,
+                                        const uint8_t* ws, int64_t row0, int rows, int64_t n0, int64_t N, int64_t K, int KB) {
+    constexpr int U = 4;                     // loads of 64 elements in flight: two scale blocks of each weight row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = (lane & 3) * 16;
+    const uint8_t* w0 = n0 + g < N ? we + (n0 + g) * K : nullptr;
+    const uint8_t* w1 = n0 + g + 8 < N ? we + (n0 + g + 8) * K : nullptr;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    float total[NTT][4] = {};
+    for (int64_t k0 = warp * 256; k0 < K; k0 += FEW_WARPS * 256) {
+        uint4 wa[U], wb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + 64 * u + q;
+            Vec<4> x{{0, 0, 0, 0}}, y{{0, 0, 0, 0}};
+            if (k < K && w0) x = ld_stream<4, true>((const Vec<4>*)(w0 + k));
+            if (k < K && w1) y = ld_stream<4, true>((const Vec<4>*)(w1 + k));
+            wa[u] = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+            wb[u] = make_uint4(y.w[0], y.w[1], y.w[2], y.w[3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {        // scale blocks
+            const int kb = (int)(k0 >> 7) + h;
+            if (kb >= KB) break;
+            const uint32_t ew = __ldg(ws + kb);
+            float acc[NTT][4] = {};
+#pragma unroll
+            for (int u = 2 * h; u < 2 * h + 2; ++u) {
+                const int64_t k = k0 + 64 * u + q;
+                const uint32_t* x = (const uint32_t*)&wa[u];
+                const uint32_t* y = (const uint32_t*)&wb[u];
+                uint4 t[NTT];
+#pragma unroll
+                for (int i = 0; i < NTT; ++i)
+                    t[i] = (k < K && 8 * i + g < rows) ? __ldg((const uint4*)(a + (row0 + 8 * i + g) * K + k)) : zero;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t a0 = half2_of(x[s]), a2 = half2_of(x[s] >> 16);
+                    const uint32_t a1 = half2_of(y[s]), a3 = half2_of(y[s] >> 16);
+#pragma unroll
+                    for (int i = 0; i < NTT; ++i) {
+                        const uint32_t v = ((const uint32_t*)&t[i])[s];
+                        mma_f16(acc[i], a0, a1, a2, a3, half2_of(v), half2_of(v >> 16));
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NTT; ++i) {  // acc: (weight row g, rows 2(lane % 4), +1), (weight row g + 8, ..)
+                const int r = 8 * i + 2 * (lane & 3);
+                const float2 f0 = scale_factors(r < rows ? __ldg(as + (row0 + r) * KB + kb) : 127u, ew);
+                const float2 f1 = scale_factors(r + 1 < rows ? __ldg(as + (row0 + r + 1) * KB + kb) : 127u, ew);
+                total[i][0] += acc[i][0] * f0.x * f0.y;
+                total[i][1] += acc[i][1] * f1.x * f1.y;
+                total[i][2] += acc[i][2] * f0.x * f0.y;
+                total[i][3] += acc[i][3] * f1.x * f1.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NTT; ++i) {
+        const int r = 8 * i + 2 * (lane & 3);
+        sh.part[warp][r][g] = total[i][0];
+        sh.part[warp][r + 1][g] = total[i][1];
+        sh.part[warp][r][g + 8] = total[i][2];
+        sh.part[warp][r + 1][g + 8] = total[i][3];
+    }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(FEW_WARPS * 32, 3)
+    linear_fp8_few_kernel(const uint8_t* __restrict__ a, const uint8_t* __restrict__ as, const uint8_t* __restrict__ w,
+                          const uint8_t* __restrict__ ws, const int64_t* __restrict__ offsets, const float* __restrict__ bias,
+                          const uint16_t* __restrict__ residual, void* __restrict__ out, int out_fp32,
+                          uint16_t* __restrict__ pre, int E, int64_t R, int64_t N, int64_t K) {
+    __shared__ FewShared sh;
+    __shared__ int tile_start[MAX_EXPERTS + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // first job of each expert: ceil(rows / FEW_ROWS) each
+    if (threadIdx.x == 0) tile_start[0] = 0;
+    const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) {
+        tile_start[e + 1] = (int)((en - b + FEW_ROWS - 1) / FEW_ROWS);
+    });
+    if (!orderly) drop_overlapping(offsets, E, R, tile_start + 1, nullptr);
+    if (warp == 0) prefix_in_place(tile_start, E, lane);
+    __syncthreads();
+    const int T = tile_start[E];
+    const int groups = (int)((N + 15) / 16), KB = (int)((K + KB8 - 1) / KB8), NB = (int)((N + QBLOCK - 1) / QBLOCK);
+    const int64_t jobs = (int64_t)T * groups;
+    for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
+        const int t = (int)(j / groups);
+        const int64_t n0 = (int64_t)(j - (int64_t)t * groups) * 16;
+        int lo = 0, hi = E - 1;              // last e with tile_start[e] <= t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+        }
+        int64_t b, en;
+        expert_range(offsets, lo, R, b, en);
+        const int64_t row0 = b + (int64_t)(t - tile_start[lo]) * FEW_ROWS;
+        const int rows = (int)min((int64_t)FEW_ROWS, en - row0);
+        const uint8_t* we = w + (int64_t)lo * N * K;
+        const uint8_t* se = ws + ((int64_t)lo * NB + n0 / QBLOCK) * KB;
+        if (rows <= 8) few_job<1>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
+        else if (rows <= 16) few_job<2>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
+        else few_job<4>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * 16; i += blockDim.x) {
+            const int r = i >> 4, c = i & 15;
+            const int64_t n = n0 + c;
+            if (n >= N) continue;
+            float z = 0.0f;
+#pragma unroll
+            for (int k = 0; k < FEW_WARPS; ++k) z += sh.part[k][r][c];
+            if (bias) z += bias[(int64_t)lo * N + n];
+            const int64_t at = (row0 + r) * N + n;
+            if (pre) pre[at] = f32_to_bf16(z);
+            float y = act_value<ACT>(z);
+            if (residual) y += bf16_to_f32(residual[at]);
+            if (out_fp32) ((float*)out)[at] = y;
+            else ((uint16_t*)out)[at] = f32_to_bf16(y);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+// Up to how many rows linear_fp8_few_kernel takes the forward: on average two an expert, or 64 in all.
+constexpr int64_t FEW_MAX_MEAN_ROWS = 2;
+constexpr int64_t FEW_MAX_ROWS = 64;
+
+struct Args {
+    const uint8_t *a, *as, *w, *ws;
+    const int64_t* offsets;
+    int64_t E;
+    const float* bias;
+    const void* residual;
+    void* out;
+    bool out_fp32;
+    void* pre;
+    int* status;
+    int64_t R, N, K;
+    cudaStream_t stream;
+};
+
+// NCOL output columns (N forward, K dgrad), KC the contraction.
+template <bool W_MN, int ACT>
+int launch_tc(const Args& p) {
+    const int64_t NCOL = W_MN ? p.K : p.N, KC = W_MN ? p.N : p.K;
+    CUtensorMap map_w;
+    RowMaps map_r;
+    const uint64_t rdims[2] = {(uint64_t)KC, (uint64_t)p.R}, rstride[1] = {(uint64_t)KC};
+    for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t box[2] = {KB8, 128u >> i};
+        if (!make_map_bytes(&map_r.m[i], p.a, 2, rdims, rstride, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
+            return cuda_fail(cudaErrorInvalidValue);
+    }
+    // [E, N, K] as stored
+    const uint64_t dims[3] = {(uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.E}, strides[2] = {(uint64_t)p.K, (uint64_t)(p.N * p.K)};
+    const uint32_t box[3] = {128, 128, 1};
+    const CUtensorMapL2promotion promo = p.K % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+    if (!make_map_bytes(&map_w, p.w, 3, dims, strides, box, promo)) return cuda_fail(cudaErrorInvalidValue);
+    int sms = 0;
+    const int st = sm_count(&sms);
+    if (st != SITU_GLU_OK) return st;
+    const int NT = (int)((NCOL + TILE - 1) / TILE);
+    const int64_t KB = (KC + KB8 - 1) / KB8;
+    const int most = pick_chunk(p.R, p.E, NT, KB, sms / 2, MAX_CHUNK);
+    const int64_t jobs = ((p.R + most - 1) / most + p.E - 1) * NT;   // at most: every expert's last chunk partial
+    if (jobs > INT32_MAX - 2 * sms) return SITU_GLU_INVALID_ARG;     // the kernel counts them in 32 bits
+    const int nb = (int)((p.N + QBLOCK - 1) / QBLOCK), kb = (int)((p.K + QBLOCK - 1) / QBLOCK);
+    const ScaleStrides ss = {(int64_t)nb * kb, W_MN ? 1 : kb, W_MN ? kb : 1, W_MN ? kb : nb};
+    const cudaError_t e = launch_pairs(linear_fp8_tc_kernel<W_MN, ACT>, jobs, NUM_THREADS, SMEM_BYTES, p.stream, map_w, map_r, p.as,
+                                       p.ws, ss, p.offsets, p.bias, (const uint16_t*)p.residual, p.out, p.out_fp32 ? 1 : 0,
+                                       (uint16_t*)p.pre, p.status, (int)p.E, p.R, NCOL, (int)KB, most);
+    return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
+}
+
+template <int ACT>
+int launch_few(const Args& p) {
+    auto kernel = linear_fp8_few_kernel<ACT>;
+    // one warp of work per row as grid_for counts it: every 16 weight rows of every possible job
+    int grid = 0;
+    const int64_t tiles = p.R < p.E ? p.R : (p.R + FEW_ROWS - 1) / FEW_ROWS + p.E;
+    const int st = grid_for((const void*)kernel, FEW_WARPS * 32, tiles * ((p.N + 15) / 16) * FEW_WARPS, &grid);
+    if (st != SITU_GLU_OK) return st;
+    kernel<<<grid, FEW_WARPS * 32, 0, p.stream>>>(p.a, p.as, p.w, p.ws, p.offsets, p.bias, (const uint16_t*)p.residual, p.out,
+                                                  p.out_fp32 ? 1 : 0, (uint16_t*)p.pre, (int)p.E, p.R, p.N, p.K);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
+}
+
+template <int ACT>
+int launch_fwd(const Args& p) {
+    return p.R <= FEW_MAX_ROWS || p.R <= p.E * FEW_MAX_MEAN_ROWS ? launch_few<ACT>(p) : launch_tc<false, ACT>(p);
+}
+
+int check_fp8(int64_t E, const void* offsets, int64_t R, int64_t N, int64_t K) {
+    if (N % 16 != 0 || K % 16 != 0) return SITU_GLU_INVALID_ARG;     // TMA: rows of codes are multiples of 16 bytes
+    return check_linear(E, offsets, R, N, K);
+}
+
+int64_t nblocks(int64_t n) { return (n + QBLOCK - 1) / QBLOCK; }
+
+}  // namespace
+
+extern "C" {
+
+int situ_linear_fp8_fwd(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales,
+                        const int64_t* expert_offsets, int64_t E, const float* bias, const void* residual, int act, void* out,
+                        int out_type, void* pre, int* status, int64_t R, int64_t N, int64_t K, cudaStream_t stream) {
+    const int st = check_fp8(E, expert_offsets, R, N, K);
+    if (st != SITU_GLU_OK) return st;
+    if (act < SITU_ACT_NONE || act > SITU_ACT_GELU || (out_type != SITU_BF16 && out_type != SITU_FP32))
+        return SITU_GLU_INVALID_ARG;
+    if (R == 0) return SITU_GLU_OK;
+    if (!a || !a_scales || !w || !w_scales || !out) return SITU_GLU_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(residual, 16) || !aligned(pre, 16) ||
+        !aligned(bias, 4) || !aligned(expert_offsets, 8) || !aligned(status, 4))
+        return SITU_GLU_INVALID_ARG;
+    const int64_t osz = out_type == SITU_FP32 ? 4 : 2;
+    const Range in[7] = {range_of(a, R * K), range_of(a_scales, R * nblocks(K)), range_of(w, E * N * K),
+                         range_of(w_scales, E * nblocks(N) * nblocks(K)), range_of(bias, bias ? E * N * 4 : 0),
+                         range_of(residual, residual ? R * N * 2 : 0),
+                         range_of(expert_offsets, expert_offsets ? (E + 1) * 8 : 0)};
+    const Range o[3] = {range_of(out, R * N * osz), range_of(pre, pre ? R * N * 2 : 0), range_of(status, status ? 4 : 0)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (overlap(o[i], r)) return SITU_GLU_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (overlap(o[i], o[j])) return SITU_GLU_OVERLAP;
+    }
+    const Args p = {a, a_scales, w, w_scales, expert_offsets, E, bias, residual, out, out_type == SITU_FP32, pre, status, R, N, K, stream};
+    switch (act) {
+        case SITU_ACT_RELU: return launch_fwd<SITU_ACT_RELU>(p);
+        case SITU_ACT_SILU: return launch_fwd<SITU_ACT_SILU>(p);
+        case SITU_ACT_GELU: return launch_fwd<SITU_ACT_GELU>(p);
+        default: return launch_fwd<SITU_ACT_NONE>(p);
+    }
+}
+
+int situ_linear_fp8_dgrad(const uint8_t* dz, const uint8_t* dz_scales, const uint8_t* w, const uint8_t* w_scales,
+                          const int64_t* expert_offsets, int64_t E, void* da, int* status, int64_t R, int64_t N, int64_t K,
+                          cudaStream_t stream) {
+    const int st = check_fp8(E, expert_offsets, R, N, K);
+    if (st != SITU_GLU_OK) return st;
+    if (R == 0) return SITU_GLU_OK;
+    if (!dz || !dz_scales || !w || !w_scales || !da) return SITU_GLU_INVALID_ARG;
+    if (!aligned(dz, 16) || !aligned(w, 16) || !aligned(da, 16) || !aligned(expert_offsets, 8) || !aligned(status, 4))
+        return SITU_GLU_INVALID_ARG;
+    const Range rda = range_of(da, R * K * 2), rs = range_of(status, status ? 4 : 0);
+    for (const Range& r : {range_of(dz, R * N), range_of(dz_scales, R * nblocks(N)), range_of(w, E * N * K),
+                           range_of(w_scales, E * nblocks(N) * nblocks(K)),
+                           range_of(expert_offsets, expert_offsets ? (E + 1) * 8 : 0)})
+        if (overlap(rda, r) || overlap(rs, r)) return SITU_GLU_OVERLAP;
+    if (overlap(rda, rs)) return SITU_GLU_OVERLAP;
+    return launch_tc<true, SITU_ACT_NONE>({dz, dz_scales, w, w_scales, expert_offsets, E, nullptr, nullptr, da, false, nullptr,
+                                           status, R, N, K, stream});
+}
+
+}  // extern "C"

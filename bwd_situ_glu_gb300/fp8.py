@@ -2,6 +2,9 @@
 
 * ``situ_quant_fp8`` / ``situ_dequant_fp8``: E4M3 codes with a power-of-two scale for each 128 elements of a row, or
   128 x 128 of a weight
+* ``situ_linear_fp8`` / ``situ_linear_fp8_bwd``: the product of quantised rows and weights, per expert or dense, with bias,
+  activation and residual, and its gradients
+* ``linear_fp8``: the same as an autograd operator of bf16 rows and a bf16 or fp32 weight
 
 A quantised tensor is a pair (codes uint8, scale bytes uint8): a byte b stands for 2^(b-127). ``codes.view(torch.float8_e4m3fn)``
 are the codes' values. The conventions are those of the module ``moe``.
@@ -10,8 +13,9 @@ from __future__ import annotations
 
 import torch
 
-from bwd_situ_glu_gb300 import _check, load as _lib
-from bwd_situ_glu_gb300.moe import _device_now, _elsewhere, _empty, _need, _out, _raw_stream, _type, _CODE, _BF16
+from bwd_situ_glu_gb300 import _check, load as _lib, moe
+from bwd_situ_glu_gb300.moe import (_act, _device_now, _elsewhere, _empty, _need, _out, _ptr, _raw_stream, _scratch, _two, _type,
+                                    _BF16, _CODE, _F32, _I32, _I64)
 
 _U8 = torch.uint8
 BLOCK = 128   # elements of a row (or rows and columns of a weight) that share a scale
@@ -73,3 +77,175 @@ def situ_dequant_fp8(codes, scales, block_rows=1, dtype=None, out=None, stream=N
     _check(_lib().situ_dequant_fp8(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), _CODE[dtype], E, R, D, block_rows,
                                    _raw_stream(dev.index)))
     return out
+
+
+# ---------------------------------------------------------------- linear
+
+def _pair(t, name):
+    """(codes, scales) of a quantised tensor."""
+    if not isinstance(t, (tuple, list)) or len(t) != 2 or not all(isinstance(x, torch.Tensor) for x in t):
+        raise TypeError(f"{name} must be a pair (codes, scales) of situ_quant_fp8")
+    return t
+
+
+def _weight(w, expert_offsets, dev):
+    """(codes, scales, E, N, K, lead) of a quantised weight, [N,K] without expert_offsets, [E,N,K] with them."""
+    wq, ws = _pair(w, "w")
+    if wq.dim() != (2 if expert_offsets is None else 3):
+        raise ValueError("w must be [N, K] without expert_offsets, [E, N, K] with them")
+    lead, (N, K) = tuple(wq.shape[:-2]), wq.shape[-2:]
+    E = lead[0] if lead else 1
+    _need(wq, _U8, (*lead, N, K), dev, "w codes")
+    _need(ws, _U8, (*lead, _blocks(N), _blocks(K)), dev, "w scales")
+    if expert_offsets is not None:
+        _need(expert_offsets, _I64, (E + 1,), dev, "expert_offsets")
+    return wq, ws, E, N, K, lead
+
+
+def situ_linear_fp8(a, w, expert_offsets=None, bias=None, residual=None, act="none", save_pre=False, out=None, out_dtype=None,
+                    status=None, stream=None):
+    """situ_linear with rows and weights in 8 bits: out [R,N] = act(a W_eT + b_e) + residual. a: (codes [R,K], scales) of
+    situ_quant_fp8, or a bf16 or fp32 tensor [R,K], which is quantised first; w: (codes [E,N,K] or [N,K], scales) of
+    situ_quant_fp8 with block_rows 128. The other arguments are those of situ_linear. N and K multiples of 16."""
+    plain = isinstance(a, torch.Tensor)
+    aq, as_ = (a, None) if plain else _pair(a, "a")
+    R, dev = _two(aq, "a")[0], aq.device
+    wq, ws, E, N, K, lead = _weight(w, expert_offsets, dev)
+    if plain:
+        _type(a, "a")
+        _need(a, a.dtype, (R, K), dev, "a")
+    else:
+        _need(aq, _U8, (R, K), dev, "a codes")
+        _need(as_, _U8, (R, _blocks(K)), dev, "a scales")
+    if bias is not None:
+        _need(bias, _F32, (*lead, N), dev, "bias")
+    if residual is not None:
+        _need(residual, _BF16, (R, N), dev, "residual")
+    if status is not None:
+        _need(status, _I32, (1,), dev, "status")
+    code = _act(act)
+    if stream is not None or dev.index != _device_now():
+        return _elsewhere(stream, aq, lambda: situ_linear_fp8(a, w, expert_offsets, bias, residual, act, save_pre, out,
+                                                              out_dtype, status))
+    if out is not None:
+        out_dtype = out.dtype
+    out = _out(out, (R, N), out_dtype or _BF16, dev, "out")
+    if plain:
+        aq, as_ = situ_quant_fp8(a)
+    pre = _empty((R, N), dtype=_BF16, device=dev) if save_pre else None
+    _check(_lib().situ_linear_fp8_fwd(aq.data_ptr(), as_.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(expert_offsets), E,
+                                      _ptr(bias), _ptr(residual), code, out.data_ptr(), _type(out, "out"), _ptr(pre),
+                                      _ptr(status), R, N, K, _raw_stream(dev.index)))
+    return (out, pre) if save_pre else out
+
+
+def situ_linear_fp8_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, dw_dtype=None, bias=True, need_da=True,
+                        need_dw=True, status=None, stream=None):
+    """(da bf16 [R,K], dw [E,N,K] (or [N,K]) of dw_dtype (default fp32), dbias fp32 [E,N] (or [N])) of situ_linear_fp8 for
+    dout bf16 [R,N], a and w quantised as in the forward (a is not used without need_dw). dz = dout*act'(pre), rounded to
+    bf16, as in situ_linear_bwd; da is the product of dz in 8 bits and the weights as they are; dw is the product of dz
+    and the decoded rows, which bf16 holds exactly, on bf16 operands: it feeds an optimizer. What is not asked for is
+    None. An expert without rows gets zeros in dw and dbias; da of rows of no expert is not written."""
+    R, N_ = _two(dout, "dout")
+    dev = dout.device
+    wq, ws, E, N, K, lead = _weight(w, expert_offsets, dev)
+    _need(dout, _BF16, (R, N), dev, "dout")
+    if need_dw:
+        aq, as_ = _pair(a, "a")
+        _need(aq, _U8, (R, K), dev, "a codes")
+        _need(as_, _U8, (R, _blocks(K)), dev, "a scales")
+    code = _act(act)
+    if code:
+        if pre is None:
+            raise ValueError(f"act {act!r} needs the saved pre (situ_linear_fp8 with save_pre=True)")
+        _need(pre, _BF16, (R, N), dev, "pre")
+    else:
+        pre = None
+    if status is not None:
+        _need(status, _I32, (1,), dev, "status")
+    if stream is not None or dev.index != _device_now():
+        return _elsewhere(stream, dout, lambda: situ_linear_fp8_bwd(dout, a, w, expert_offsets, act, pre, dw_dtype, bias,
+                                                                    need_da, need_dw, status))
+    lib, s = _lib(), _raw_stream(dev.index)
+    da = dw = dbias = None
+    dz, off = dout, _ptr(expert_offsets)
+    if code or bias:
+        if code:
+            dz = _empty((R, N), dtype=_BF16, device=dev)
+        nb, buf = 0, None
+        if bias:
+            dbias = _empty((*lead, N), dtype=_F32, device=dev)
+            nb = lib.situ_linear_act_bwd_workspace(R, N, E)
+            buf = _scratch(nb, dout)
+        _check(lib.situ_linear_act_bwd(dout.data_ptr(), _ptr(pre), code, off, E, dz.data_ptr() if code else 0,
+                                       _ptr(dbias), _ptr(buf), nb, R, N, s))
+    if need_da:
+        da = _empty((R, K), dtype=_BF16, device=dev)
+        dq, ds = situ_quant_fp8(dz)
+        _check(lib.situ_linear_fp8_dgrad(dq.data_ptr(), ds.data_ptr(), wq.data_ptr(), ws.data_ptr(), off, E, da.data_ptr(),
+                                         _ptr(status), R, N, K, s))
+    if need_dw:
+        dw = _empty((*lead, N, K), dtype=dw_dtype or _F32, device=dev)
+        nb = lib.situ_linear_wgrad_workspace(R, N, K, E)
+        buf = _scratch(nb, dout)
+        rows = situ_dequant_fp8(aq, as_)
+        _check(lib.situ_linear_wgrad(dz.data_ptr(), rows.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"), _ptr(buf), nb,
+                                     _ptr(status), R, N, K, s))
+    return da, dw, dbias
+
+
+# ---------------------------------------------------------------- autograd operator
+
+_function = None
+
+
+def _autograd():
+    """The autograd Function, created on first use."""
+    global _function
+    if _function is not None:
+        return _function
+    moe._autograd()
+
+    class LinearFp8(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a, w, bias, residual, expert_offsets, act, wq, status, grad):
+            # needs_input_grad goes by the inputs alone; without grad mode there is no backward to keep anything for
+            needs = grad and any(ctx.needs_input_grad[:3])
+            keep = act != "none" and needs
+            aq = situ_quant_fp8(a)
+            wq = situ_quant_fp8(w, block_rows=BLOCK) if wq is None else wq
+            out = situ_linear_fp8(aq, wq, expert_offsets, bias, residual, act, save_pre=keep, status=status)
+            out, pre = out if keep else (out, None)
+            if needs:          # the inputs only mark what the gradients depend on
+                ctx.save_for_backward(*aq, *wq, expert_offsets, pre, a if keep else None, w, bias if keep else None)
+            ctx.act, ctx.status, ctx.dw_dtype = act, status, w.dtype   # status is not saved as a tensor: the kernels write it
+            return out
+
+        @staticmethod
+        def backward(ctx, dout):
+            need = ctx.needs_input_grad
+            none = (None,) * 5
+            if not any(need[:3]):      # the residual's alone
+                return None, None, None, dout, *none
+            aq, as_, wq, ws, expert_offsets, pre, a, w, bias = ctx.saved_tensors
+            dout = dout.contiguous()
+            da, dw, db = situ_linear_fp8_bwd(dout, (aq, as_), (wq, ws), expert_offsets, ctx.act, pre, dw_dtype=ctx.dw_dtype,
+                                             bias=need[2], need_da=need[0], need_dw=need[1], status=ctx.status)
+            da, dw, db = moe._once((da, dw, db), dout, a, w, bias)
+            return da, dw, db, dout if need[3] else None, *none
+
+    _function = LinearFp8
+    return _function
+
+
+def linear_fp8(a, w, bias=None, residual=None, expert_offsets=None, act="none", wq=None, status=None):
+    """situ_linear_fp8 of bf16 rows a and a bf16 or fp32 weight w (both quantised here; ``wq``: w's codes and scales where
+    the program has them, as after an optimizer step), bf16 out, differentiable in a, w (gradient in w's type), bias and
+    residual. The gradients are those of the product of the quantised operands, taken for the operands' own (the codes'
+    rounding has no derivative). The backward keeps the rows' codes, not the rows."""
+    if wq is not None:
+        if tuple(_pair(wq, "wq")[0].shape) != tuple(w.shape):
+            raise ValueError("wq must be w's codes and scales")
+    if isinstance(a, torch.Tensor) and a.dtype != _BF16:
+        raise TypeError(f"a must be torch.bfloat16, got {a.dtype}")
+    return _autograd().apply(a, w, bias, residual, expert_offsets, act, wq, status, torch.is_grad_enabled())

@@ -338,11 +338,12 @@ def selftest_wait_timeout(status, elapsed_ns=None, stream=None):
 # ---------------------------------------------------------------- autograd operators
 
 _functions = None
+_once = None      # set by _autograd: gradients whose second derivative raises
 
 
 def _autograd():
     """The autograd Functions, created on first use."""
-    global _functions
+    global _functions, _once
     if _functions is not None:
         return _functions
 
@@ -427,6 +428,7 @@ def _autograd():
             da, dw, db = once((da, dw, db), dout, a, w, bias)
             return da, dw, db, dout if need[3] else None, None, None, None, None
 
+    _once = once
     _functions = (RouteTopk, Dispatch, Combine, Linear)
     return _functions
 

@@ -36,6 +36,25 @@ int situ_quant_fp8(const void* x, int type, uint8_t* codes, uint8_t* scales, int
 int situ_dequant_fp8(const uint8_t* codes, const uint8_t* scales, void* x, int type, int64_t E, int64_t R, int64_t D,
                      int block_rows, cudaStream_t stream);
 
+/* ---- matrix product of quantised rows and weights ------------------------------------------
+ * As situ_linear_fwd, with a [R, K] and w [E, N, K] (the nn.Linear layout) as codes and scales of
+ * situ_quant_fp8 with block_rows 1 and 128: a_scales [R, ceil(K/128)], w_scales [E, ceil(N/128),
+ * ceil(K/128)]. The products of codes and their scaling are exact, the sum over K is kept in fp32. bias, residual, act, out, pre,
+ * expert_offsets and status are those of situ_linear_fwd. N % 16 == 0, K % 16 == 0; 1 <= E <= 1024;
+ * R <= 2^31 - 1025; a, w, residual, out and pre 16-byte aligned. A NaN code or scale gives NaN in the row
+ * (of a) or the output columns (of w) that use it, nowhere else. */
+int situ_linear_fp8_fwd(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales,
+                        const int64_t* expert_offsets, int64_t E, const float* bias, const void* residual, int act, void* out,
+                        int out_type, void* pre, int* status, int64_t R, int64_t N, int64_t K, cudaStream_t stream);
+
+/* da bf16 [R, K] = dz·W_e (fp32 accumulation, rounded once) for dz [R, N] as codes and scales with block_rows 1
+ * (dz_scales [R, ceil(N/128)]); the weights' codes and scales are the forward's. The other arguments as
+ * situ_linear_fp8_fwd. (The weight gradient is situ_linear_wgrad of the unquantised dz and the decoded rows,
+ * which bf16 holds exactly.) */
+int situ_linear_fp8_dgrad(const uint8_t* dz, const uint8_t* dz_scales, const uint8_t* w, const uint8_t* w_scales,
+                          const int64_t* expert_offsets, int64_t E, void* da, int* status, int64_t R, int64_t N, int64_t K,
+                          cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
