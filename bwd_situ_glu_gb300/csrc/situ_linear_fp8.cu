@@ -8,9 +8,11 @@
 // What differs:
 //   * tcgen05.mma kind::mxf8f6f4 with block scales: the tensor core multiplies each 32-deep step of a row by a
 //     power of two held as a byte in TMEM, so the scales of 128-deep blocks cost neither instructions in the epilogue
-//     nor a rounding. A fifth role, the scale warp of each CTA, writes the bytes of a ring stage (its 128 weight
-//     rows': one byte for all; the chunk's rows': one each) in the layout that tcgen05.cp takes; the MMA warp copies them to
-//     TMEM in front of the stage's four MMAs. Each byte stands four times in a word, once for each MMA of the block.
+//     nor a rounding. A fifth role, the scale warp of each CTA, writes the bytes of four blocks at a time (its 128 weight
+//     rows': one byte for all; the chunk's rows': one each) in the layout that tcgen05.cp takes; the MMA warp copies a block's to
+//     TMEM in front of its four MMAs. Each byte stands four times in a word, once for each MMA of the block.
+//     (Handing over to the tensor core block by block, the proxy fence and the remote arrival, took longer than a
+//     block's products: 16385 x 3584 x 3584 in 380 us, four at a time 168, with the bytes fetched ahead 162.)
 //   * two accumulators and the scales share TMEM's 512 columns, so a chunk has at most 224 rows.
 //   * the dgrad reads W_e as stored (contraction apart, "MN-major"): boxes of 128 columns x 128 rows of bytes.
 //   * linear_fp8_few_kernel: for few rows per expert, as there.
@@ -48,7 +50,8 @@ constexpr int NUM_THREADS = (SCALE_WARP + 1) * 32;    // TMA, MMA, epilogue, sca
 constexpr int SCALE_PIECE = 512;
 constexpr int SCALE_BYTES = 3 * SCALE_PIECE;
 constexpr int SCALE_COL0 = 2 * ACC_COLS;     // in TMEM: 4 columns a piece
-constexpr int SCALE_SLOTS = 5;               // stages whose scales TMEM holds; the tensor core takes copies and MMAs in order
+constexpr int SCALE_SLOTS = 5;               // blocks whose scales TMEM holds; the tensor core takes copies and MMAs in order
+constexpr int GROUP_KB = 4, GROUPS = 2;      // blocks whose scales are handed over at once; such groups in shared memory
 static_assert(SCALE_COL0 + SCALE_SLOTS * 12 <= TMEM_COLS, "TMEM columns");
 
 // A ring stage: 128 weight rows and half of the chunk's rows, 128 bytes each.
@@ -59,7 +62,13 @@ __host__ __device__ constexpr int ring_stages(int most) {
     return s < PSTAGES ? s : PSTAGES;
 }
 
-constexpr int SMEM_BYTES = 1024 + RING_BYTES + PSTAGES * SCALE_BYTES + NUM_EPI_WARPS * PATCH + (int)sizeof(PairBars) + (int)sizeof(Plan);
+struct alignas(8) ScaleBars {
+    uint64_t full[GROUPS];                   // leader's: both CTAs have written a group
+    uint64_t empty[GROUPS];                  // both: the commit of the MMAs behind a group's copies
+};
+
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + GROUPS * GROUP_KB * SCALE_BYTES + NUM_EPI_WARPS * PATCH + (int)sizeof(PairBars) + (int)sizeof(ScaleBars) +
+                           (int)sizeof(Plan);
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
 // Instruction descriptor, kind::mxf8f6f4 on a pair: fp32 accumulate, E4M3 operands (formats 0), E8M0 scales (bit 23), scale
@@ -92,6 +101,10 @@ __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
 // The same fields as a K-major tile's.
 __device__ __forceinline__ uint64_t smem_desc_mn8(uint32_t saddr) { return smem_desc(saddr); }
 
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return a | (b << 8) | (c << 16) | (d << 24);
+}
+
 struct RowMaps {
     CUtensorMap m[4];                        // boxes of 128 >> i rows
 };
@@ -114,17 +127,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* scales = ring + RING_BYTES;
-    uint8_t* patches = scales + PSTAGES * SCALE_BYTES;
+    uint8_t* patches = scales + GROUPS * GROUP_KB * SCALE_BYTES;
     PairBars* bars = (PairBars*)(patches + NUM_EPI_WARPS * PATCH);
-    Plan& plan = *(Plan*)(bars + 1);
+    ScaleBars* sbars = (ScaleBars*)(bars + 1);
+    Plan& plan = *(Plan*)(sbars + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int NT = (int)((NCOL + TILE - 1) / TILE);
     const int sbytes = stage_bytes(most), stages = ring_stages(most);
 
     build_plan(plan, offsets, E, R, most);
-    // a full stage: the loads' bytes, announced by the leader's producer, and both CTAs' scales
-    const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS, 3);
+    if (threadIdx.x == 0) {                  // before pair_setup's fence and barriers
+        for (int g = 0; g < GROUPS; ++g) {
+            mbar_init(&sbars->full[g], 2);
+            mbar_init(&sbars->empty[g], 1);
+        }
+    }
+    const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS);
     const int jobs = plan.start[E] * NT;
     const int j0 = blockIdx.x >> 1, jstep = gridDim.x >> 1;
 
@@ -176,28 +195,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             bool ok = true;
             int n_next = j0 < jobs ? job_at(j0, plan, E, NT).n : 0;
             const uint32_t ring_addr = smem_addr(ring), scale_addr = smem_addr(scales);
+            // The scales of the block after the one that was copied last, over the jobs: one block ahead of the products, which
+            // otherwise wait for each copy.
+            int cj = j0, ckb = 0, cslot = 0, group = 0;
+            uint32_t gphase = 0;
+            auto copy_next = [&]() {
+                if (cj >= jobs) return true;
+                const int k = ckb % GROUP_KB;
+                if (k == 0) {
+                    if (!pair_wait<true>(&sbars->full[group], gphase, &bars->abort, status)) return false;
+                    tc_fence_after();
+                }
+                const bool end = ckb + 1 == KB, last = end || k == GROUP_KB - 1;     // of the job, of the group
+                if (elected) {
+                    const uint64_t sd = scale_desc(scale_addr + (uint32_t)((group * GROUP_KB + k) * SCALE_BYTES));
+                    const uint32_t at = tmem + (uint32_t)(SCALE_COL0 + cslot * 12);
+                    copy_scales(at, sd);
+                    copy_scales(at + 4, sd + (SCALE_PIECE >> 4));
+                    copy_scales(at + 8, sd + 2 * (SCALE_PIECE >> 4));
+                    if (last) pair_commit(&sbars->empty[group]);
+                }
+                if (last && ++group == GROUPS) { group = 0; gphase ^= 1; }
+                if (++cslot == SCALE_SLOTS) cslot = 0;
+                ++ckb;
+                if (end) { ckb = 0; cj += jstep; }
+                return true;
+            };
+            ok = copy_next();
             for (int j = j0; ok && j < jobs; j += jstep, ++job) {
-                const int n = n_next;
-                const uint32_t idesc = scaled_idesc(n, W_MN);
+                const uint32_t idesc = scaled_idesc(n_next, W_MN);
                 const int acc = job & 1;
                 const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
                 if (!pair_wait<true>(&bars->tempty[acc], (uint32_t)((job >> 1) & 1) ^ 1, &bars->abort, status)) break;
                 tc_fence_after();
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!pair_wait<true>(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
+                    if (!pair_wait(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sa = ring_addr + (uint32_t)(stage * sbytes);
                     const uint64_t ad = W_MN ? smem_desc_mn8(sa) : smem_desc(sa), bd = smem_desc(sa + PA_BYTES);
-                    const uint64_t sd = scale_desc(scale_addr + (uint32_t)(stage * SCALE_BYTES));
                     const uint32_t sft = tmem + (uint32_t)(SCALE_COL0 + slot * 12);
+                    if (elected) scaled_mma(d, ad, bd, idesc, sft, sft + 4, (uint32_t)kb);
+                    if (!copy_next()) { ok = false; break; }
                     if (elected) {
-                        copy_scales(sft, sd);
-                        copy_scales(sft + 4, sd + (SCALE_PIECE >> 4));
-                        if (n > 128) copy_scales(sft + 8, sd + 2 * (SCALE_PIECE >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < KB8 / UK8; ++kk)   // 32 deep: 32 bytes along a row, 4096 bytes MN-major
-                            scaled_mma(d, ad + (uint64_t)(kk * (W_MN ? 256 : 2)), bd + (uint64_t)(kk * 2), idesc, sft, sft + 4,
-                                       kk > 0 ? 1u : (uint32_t)kb);
+                        for (int kk = 1; kk < KB8 / UK8; ++kk)   // 32 deep: 32 bytes along a row, 4096 bytes MN-major
+                            scaled_mma(d, ad + (uint64_t)(kk * (W_MN ? 256 : 2)), bd + (uint64_t)(kk * 2), idesc, sft, sft + 4, 1u);
                         pair_commit(&bars->empty[stage]);
                     }
                     if (++stage == stages) { stage = 0; phase ^= 1; }
@@ -211,37 +253,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     } else if (warp == SCALE_WARP) {
         // ------------------------------------------------ scales (both CTAs): lane l has rows l, l + 32, .. of the chunk
-        int stage = 0;
+        int group = 0;
         uint32_t phase = 0;
         bool ok = true;
+        const bool words = KB % 4 == 0 && (uintptr_t)row_scales % 4 == 0;
         for (int j = j0; ok && j < jobs; j += jstep) {
             const Job q = job_at(j, plan, E, NT);
             const int cb = q.nt * 2 + rank;                      // this CTA's block of output columns
             const uint8_t* wp = w_scales + q.e * ws.per_expert + (int64_t)cb * ws.col_step;
             const uint8_t* rp = row_scales + (int64_t)(q.row0 + lane) * KB;
-            uint32_t b[8];
-            uint32_t wb;
+            // A group's bytes, as loaded (a word of a row, or its bytes apart), a group ahead: they are not touched before the next
+            // turn, which would wait for them here. 127 (a factor of 1) where there is nothing.
+            uint32_t raw_w[GROUP_KB], raw[7][GROUP_KB];
             auto fetch = [&](int kb) {
-                wb = cb < ws.col_blocks ? __ldg(wp + (int64_t)kb * ws.k_step) : 127u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[i] = lane + 32 * i < q.rows ? __ldg(rp + (int64_t)(32 * i) * KB + kb) : 127u;
+                for (int k = 0; k < GROUP_KB; ++k) {
+                    raw_w[k] = 127u;
+                    if (cb < ws.col_blocks && kb + k < KB) raw_w[k] = __ldg(wp + (int64_t)(kb + k) * ws.k_step);
+                }
+#pragma unroll
+                for (int i = 0; i < 7; ++i) {
+                    const bool live = lane + 32 * i < q.rows;
+                    const uint8_t* p = rp + (int64_t)(32 * i) * KB + kb;
+                    raw[i][0] = 0x7F7F7F7Fu;
+                    if (words) {
+                        if (live) raw[i][0] = __ldg((const uint32_t*)p);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < GROUP_KB; ++k) {
+                            raw[i][k] = 127u;
+                            if (live && kb + k < KB) raw[i][k] = __ldg(p + k);
+                        }
+                    }
+                }
             };
             fetch(0);
-            for (int kb = 0; kb < KB; ++kb) {
-                uint32_t v[8];
+            for (int kb = 0; kb < KB; kb += GROUP_KB) {
+                uint32_t b[7];
+                const uint32_t wb = bytes4(raw_w[0], raw_w[1], raw_w[2], raw_w[3]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = b[i] * 0x01010101u;
-                const uint32_t w = wb * 0x01010101u;
-                if (kb + 1 < KB) fetch(kb + 1);
-                if (!pair_wait(&bars->empty[stage], phase ^ 1, &bars->abort, status)) { ok = false; break; }
-                uint8_t* at = scales + stage * SCALE_BYTES + lane * 16;
-                st_shared_v4(at, w, w, w, w);
-                st_shared_v4(at + SCALE_PIECE, v[0], v[1], v[2], v[3]);
-                st_shared_v4(at + 2 * SCALE_PIECE, v[4], v[5], v[6], v[7]);
+                for (int i = 0; i < 7; ++i) b[i] = words ? raw[i][0] : bytes4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]);
+                if (kb + GROUP_KB < KB) fetch(kb + GROUP_KB);
+                if (!pair_wait(&sbars->empty[group], phase ^ 1, &bars->abort, status)) { ok = false; break; }
+                uint8_t* at = scales + group * GROUP_KB * SCALE_BYTES + lane * 16;
+#pragma unroll
+                for (int k = 0; k < GROUP_KB; ++k) {
+                    if (kb + k >= KB) break;
+                    uint32_t v[7];
+#pragma unroll
+                    for (int i = 0; i < 7; ++i) v[i] = __byte_perm(b[i], 0, k * 0x1111);
+                    const uint32_t w = __byte_perm(wb, 0, k * 0x1111);
+                    st_shared_v4(at + k * SCALE_BYTES, w, w, w, w);
+                    st_shared_v4(at + k * SCALE_BYTES + SCALE_PIECE, v[0], v[1], v[2], v[3]);
+                    st_shared_v4(at + k * SCALE_BYTES + 2 * SCALE_PIECE, v[4], v[5], v[6], 0x7F7F7F7Fu);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars->full[stage], 0));
-                if (++stage == stages) { stage = 0; phase ^= 1; }
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&sbars->full[group], 0));
+                if (++group == GROUPS) { group = 0; phase ^= 1; }
             }
         }
     } else {

@@ -156,13 +156,12 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
         : "memory");
 }
 
-// All threads of both CTAs: barriers, TMEM (512 columns), cluster barrier. epi_warps: epilogue warps per CTA;
-// full_arrivals: arrivals at a full barrier besides the loads' bytes (the leader's producer, and others that fill a stage).
-__device__ __forceinline__ uint32_t pair_setup(PairBars* bars, int epi_warps, int full_arrivals = 1) {
+// All threads of both CTAs: barriers, TMEM (512 columns), cluster barrier. epi_warps: epilogue warps per CTA.
+__device__ __forceinline__ uint32_t pair_setup(PairBars* bars, int epi_warps) {
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < PSTAGES; ++s) {
-            mbar_init(&bars->full[s], (uint32_t)full_arrivals);
+            mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 1);
             mbar_init(&bars->tail_full[s], 1);
             mbar_init(&bars->tail_ready[s], 2);
