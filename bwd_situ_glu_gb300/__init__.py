@@ -23,6 +23,8 @@ Binding names match the C entry points:
 * ``situ_quant_fp8`` / ``situ_dequant_fp8``: E4M3 codes with power-of-two scales of 128-element blocks, and
   ``situ_linear_fp8`` / ``situ_linear_fp8_bwd``: the products of such rows and weights (module ``fp8``; C ABI
   ``include/situ_fp8.h``)
+* ``AdamWPlan``, ``situ_adamw_step``: the AdamW step over many tensors on the device, states in fp32 or in 8 bits (module
+  ``adamw``; C ABI ``include/situ_adamw.h``)
 * ``situ_and_mul(x, beta, linear_beta)``: autograd function (forward kernel; backward kernel
   with p = 1), the pages' operator interface
 
@@ -47,12 +49,12 @@ LIB_PATH = os.path.join(LIB_DIR, "libsitu_glu.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("situ_glu.cu", "situ_glu_fp8.cu", "situ_glu_dgrad.cu",
                                              "situ_glu_gateup.cu", "situ_adam.cu", "situ_glu_selftest.cu", "situ_route.cu",
                                              "situ_dispatch.cu", "situ_linear.cu", "situ_linear_bwd.cu", "situ_quant.cu",
-                                             "situ_linear_fp8.cu")]
+                                             "situ_linear_fp8.cu", "situ_adamw.cu")]
 # per-source extra flags: the host Adam update is a fixed sequence of IEEE fp32 operations
 SOURCE_FLAGS = {"situ_adam.cu": ["-Xcompiler", "-ffp-contract=off,-fno-fast-math,-fno-math-errno"]}
 DEPENDS = SOURCES + [os.path.join(CSRC, n) for n in ("situ_math.cuh", "situ_device.cuh", "situ_host.h",
                                                      "situ_tc.cuh", "situ_pair.cuh", "situ_linear.cuh", "situ_linear_tc.cuh", "situ_fp8.cuh")] + [
-    os.path.join(INCLUDE, n) for n in ("situ_glu.h", "situ_moe.h", "situ_fp8.h")]
+    os.path.join(INCLUDE, n) for n in ("situ_glu.h", "situ_moe.h", "situ_fp8.h", "situ_adamw.h")]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
@@ -161,7 +163,7 @@ def load():
 
 
 def _declare_moe(lib):
-    """ctypes signatures of include/situ_moe.h and situ_fp8.h; here, so that loading the library does not import torch."""
+    """ctypes signatures of include/situ_moe.h, situ_fp8.h and situ_adamw.h; here, so that loading the library does not import torch."""
     vp, i64, cint = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     for name, args, ret in (
             ("situ_route_topk", [vp, cint, vp, vp, i64, i64, i64, vp], cint),
@@ -180,6 +182,8 @@ def _declare_moe(lib):
             ("situ_dequant_fp8", [vp, vp, vp, cint, i64, i64, i64, cint, vp], cint),
             ("situ_linear_fp8_fwd", [vp, vp, vp, vp, vp, i64, vp, vp, cint, vp, cint, vp, vp, i64, i64, i64, vp], cint),
             ("situ_linear_fp8_dgrad", [vp, vp, vp, vp, vp, i64, vp, vp, i64, i64, i64, vp], cint),
+            ("situ_adamw_coefficients_of", [ctypes.POINTER(AdamParams), ctypes.c_uint32, vp], cint),
+            ("situ_adamw_step", [vp, i64, cint, cint, ctypes.POINTER(AdamParams), ctypes.c_uint32, vp, vp, vp], cint),
             ("situ_linear_selftest_wait_timeout", [vp, vp, vp], cint),
             ("situ_linear_wgrad", [vp, vp, vp, i64, vp, cint, vp, i64, vp, i64, i64, i64, vp], cint)):
         fn = getattr(lib, name)
@@ -544,11 +548,12 @@ def situ_adam_stream_step(grad, weight, master, m, v, params: AdamParams, stagin
 _MOE_NAMES = ("situ_route_topk", "situ_route_topk_bwd", "situ_dispatch_plan", "situ_dispatch", "situ_combine",
               "situ_combine_bwd", "situ_linear", "situ_linear_bwd")
 _FP8_NAMES = ("situ_quant_fp8", "situ_dequant_fp8", "situ_linear_fp8", "situ_linear_fp8_bwd")
-_MODULES = {"moe": _MOE_NAMES, "fp8": _FP8_NAMES}
+_ADAMW_NAMES = ("AdamWPlan", "adamw_state", "adamw_coefficients", "situ_adamw_step")
+_MODULES = {"moe": _MOE_NAMES, "fp8": _FP8_NAMES, "adamw": _ADAMW_NAMES}
 
 
 def __getattr__(name):
-    """The operators around the activation live in the modules ``moe`` and ``fp8``, which import torch: on first use."""
+    """The operators around the activation live in the modules ``moe``, ``fp8`` and ``adamw``, which import torch: on first use."""
     for module, names in _MODULES.items():
         if name == module or name in names:
             m = importlib.import_module(f"{__name__}.{module}")
