@@ -115,18 +115,24 @@ class AdamWPlan:
         kind = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
         if kind not in _CODE:
             raise TypeError(f"grads must be torch.float32 or torch.bfloat16 tensors, got {kind}")
-        # a parameter's .data may have been replaced since: checked like the gradients, each time
-        for i, (g, p, shape) in enumerate(zip(grads, self._params, self._shapes)):
-            if not (isinstance(g, torch.Tensor) and g.dtype is kind and g.shape == shape and g.is_contiguous() and g.device == dev):
+        # a parameter's .data may have been replaced since: checked like the gradients, each time. (One pass of a list per
+        # property takes half the time of one pass with all of them: 64 tensors 75 -> 50 us a step.)
+        at, ps = dev.index, self._params
+        if not (all([isinstance(g, torch.Tensor) for g in grads]) and [g.shape for g in grads] == self._shapes
+                and all([g.dtype is kind for g in grads]) and all([g.get_device() == at for g in grads])
+                and all([g.is_contiguous() for g in grads])):
+            for i, (g, shape) in enumerate(zip(grads, self._shapes)):
                 _sg._need(g, kind, shape, f"grads[{i}]")
-                raise ValueError("all tensors must be on the same device")
-            if not (p.dtype is _F32 and p.shape == shape and p.is_contiguous() and p.device == dev):
+            raise ValueError("all tensors must be on the same device")
+        if not ([p.shape for p in ps] == self._shapes and all([p.dtype is _F32 for p in ps])
+                and all([p.get_device() == at for p in ps]) and all([p.is_contiguous() for p in ps])):
+            for i, (p, shape) in enumerate(zip(ps, self._shapes)):
                 _sg._need(p, _F32, shape, f"params[{i}]")
-                raise ValueError("all tensors must be on the same device")
+            raise ValueError("all tensors must be on the same device")
         if stream is not None or dev.index != _device_now():
             return _elsewhere(stream, self._params[0], lambda: self.step(grads, params, seed, grad_scale))
         table = self._table
-        table[:, 0] = [p.data_ptr() for p in self._params]
+        table[:, 0] = [p.data_ptr() for p in ps]
         table[:, 1] = [g.data_ptr() for g in grads]
         if not on_device and seed is None:
             seed = params.step

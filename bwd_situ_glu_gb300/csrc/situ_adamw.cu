@@ -24,9 +24,12 @@ using namespace situ;
 using namespace situ_host;
 using namespace situ_fp8;
 
-constexpr int TPB = 256;
+// Instructions bound the step with states in 8 bits (some 85 an element: its IEEE root and quotient, the two codes, the random
+// bits), so what counts is how many warps an SM has to choose from and how often a block's setup is paid: 201M elements in
+// 128-thread blocks, 10 an SM, 8 passes, 534 us (0.90 of the copy rate); 256 threads and 4 passes 614, one pass 732.
+constexpr int TPB = 128, BLOCKS_PER_SM = 10;
 constexpr int STEP = TPB * 8;                // elements of one pass of a block
-constexpr int PASSES = 4;
+constexpr int PASSES = 8;
 constexpr int CHUNK = STEP * PASSES;         // elements of a block: a multiple of 128
 
 struct Entry {
@@ -57,17 +60,57 @@ __host__ __device__ inline uint32_t mix(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// E4M3 code of |y| <= 448 (or not finite), rounded at random by 16 bits: as fp32 with the exponent moved to E4M3's, the
-// code is the bits above the lowest 20, for subnormal codes as for normal ones.
-__device__ __forceinline__ uint32_t random_code(float y, uint32_t bits16) {
-    const float a = fabsf(y);
-    const uint32_t z = __float_as_uint(__fmul_rn(a, 0x1p-120f));
-    const uint32_t code = min((z + (bits16 << 4)) >> 20, 0x7Eu);
-    return a < __int_as_float(0x7F800000) ? code : 0x7Fu;
+// The E4M3 code of a = |y|·2^-120, |y| <= 448, rounded at random, in the bits from 20 on: fp32 with its exponent moved to
+// E4M3's has the code above its lowest 20 bits, for subnormal codes as for normal ones. To those 16 random bits are added, and
+// four zeros.
+__device__ __forceinline__ uint32_t random_code(float a, uint32_t bits16) { return bits16 * 16u + __float_as_uint(a); }
+
+// The upper bytes of four words.
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// One moment's 8 values to codes: q (code in the upper byte), returns the block's scale byte. SHIFT: which 16 of the
+// random bits. LIFT: the values are at least 0, and what is above 0 gets a code above 0. All lanes of the warp.
+template <int SHIFT, bool LIFT>
+__device__ __forceinline__ int encode_moment(const float (&x)[8], const uint32_t (&r)[8], uint32_t (&q)[8]) {
+    uint32_t top = 0;                        // largest |x| by its bits: infinities and NaN are above all numbers
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, LIFT ? __float_as_uint(x[k]) : __float_as_uint(x[k]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const auto bits16 = [&](int k) { return SHIFT ? r[k] >> 16 : r[k] & 0xFFFFu; };
+    // 2^11 and less: |x|·2^(127-b)·2^-120 is one multiplication by a number
+    if (__all_sync(0xffffffffu, top < 0x45000000u)) {
+        const int b = scale_byte(__uint_as_float(top));
+        const float f = __uint_as_float((uint32_t)(134 - b) << 23);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            q[k] = random_code(__fmul_rn(fabsf(x[k]), f), bits16(k));
+            if (LIFT) q[k] = max(q[k], x[k] > 0.0f ? 1u << 20 : 0u);
+            q[k] <<= 4;
+            if (!LIFT) q[k] |= __float_as_uint(__fadd_rn(x[k], 0.0f)) & 0x80000000u;     // no sign on -0
+        }
+        return b;
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, finite_abs(x[k]));
+    const int b = scale_byte(halfwarp_max(amax));
+    const float inv = inverse_scale(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float y = __fmul_rn(x[k], inv), a = fabsf(y);
+        uint32_t c = random_code(__fmul_rn(a, 0x1p-120f), bits16(k));
+        if (LIFT && y > 0.0f) c = max(c, 1u << 20);
+        if (!(a < __int_as_float(0x7F800000))) c = 0x07F00000u;
+        q[k] = (c << 4) | (y < 0.0f ? 0x80000000u : 0u);
+    }
+    return b;
 }
 
 template <bool BF16_GRAD, bool EIGHT, int CAP>
-__global__ void __launch_bounds__(TPB)
+__global__ void __launch_bounds__(TPB, BLOCKS_PER_SM)
     adamw_kernel(const __grid_constant__ Table<CAP> table, const Coefs given, const Coefs* __restrict__ from_device,
                  const float* __restrict__ grad_scale) {
     int lo = 0, hi = table.count - 1;        // last tensor whose first block is <= this one
@@ -143,7 +186,6 @@ __global__ void __launch_bounds__(TPB)
                 v[k] = __fmul_rn(v[k], v[k]);
             }
         }
-        float amax_m = 0.0f, amax_v = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (grad_scale) g[k] = __fmul_rn(g[k], gs);
@@ -154,35 +196,21 @@ __global__ void __launch_bounds__(TPB)
             w[k] = __fsub_rn(__fmul_rn(w[k], c.d), __fmul_rn(c.s, __fdiv_rn(m1, q)));
             m[k] = m1;
             v[k] = EIGHT ? root : v1;
-            amax_m = fmaxf(amax_m, finite_abs(m1));
-            amax_v = fmaxf(amax_v, finite_abs(v[k]));
         }
         if constexpr (EIGHT) {               // lanes without elements hold zeros and take part
-            const int bm = scale_byte(halfwarp_max(amax_m)), bv = scale_byte(halfwarp_max(amax_v));
-            const float im = inverse_scale(bm), iv = inverse_scale(bv);
-            uint32_t qm[8], qv[8];
+            uint32_t r[8], qm[8], qv[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t r = mix((uint32_t)i0 + (uint32_t)k + c.key);
-                const float ym = __fmul_rn(m[k], im), yv = __fmul_rn(v[k], iv);
-                qm[k] = random_code(ym, r & 0xFFFFu) | (ym < 0.0f ? 0x80u : 0u);
-                qv[k] = random_code(yv, r >> 16);
-                if (yv > 0.0f && qv[k] == 0) qv[k] = 1;
-            }
+            for (int k = 0; k < 8; ++k) r[k] = mix((uint32_t)i0 + (uint32_t)k + c.key);
+            const int bm = encode_moment<0, false>(m, r, qm), bv = encode_moment<16, true>(v, r, qv);
             if (full) {
-                uint2 cm, cv;
-                cm.x = qm[0] | (qm[1] << 8) | (qm[2] << 16) | (qm[3] << 24);
-                cm.y = qm[4] | (qm[5] << 8) | (qm[6] << 16) | (qm[7] << 24);
-                cv.x = qv[0] | (qv[1] << 8) | (qv[2] << 16) | (qv[3] << 24);
-                cv.y = qv[4] | (qv[5] << 8) | (qv[6] << 16) | (qv[7] << 24);
-                *(uint2*)((uint8_t*)t.m + i0) = cm;
-                *(uint2*)((uint8_t*)t.v + i0) = cv;
+                *(uint2*)((uint8_t*)t.m + i0) = make_uint2(codes4(qm[0], qm[1], qm[2], qm[3]), codes4(qm[4], qm[5], qm[6], qm[7]));
+                *(uint2*)((uint8_t*)t.v + i0) = make_uint2(codes4(qv[0], qv[1], qv[2], qv[3]), codes4(qv[4], qv[5], qv[6], qv[7]));
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (k < live) {
-                        ((uint8_t*)t.m)[i0 + k] = (uint8_t)qm[k];
-                        ((uint8_t*)t.v)[i0 + k] = (uint8_t)qv[k];
+                        ((uint8_t*)t.m)[i0 + k] = (uint8_t)(qm[k] >> 24);
+                        ((uint8_t*)t.v)[i0 + k] = (uint8_t)(qv[k] >> 24);
                     }
             }
             if (live && i0 % QBLOCK == 0) {

@@ -36,6 +36,69 @@ __device__ __forceinline__ void chunk_values(const Chunk<F32>& c, float (&f)[8])
     }
 }
 
+// The largest magnitude of N chunks; infinities stay, and a NaN wins. Few operations an element: the ALU pipe, not HBM, bounded
+// the kernel that looked at each value by itself (65537 x 3584: 130 us).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+template <bool F32, int N>
+__device__ __forceinline__ float chunks_top(const Chunk<F32> (&c)[N]) {
+    if constexpr (F32) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(__uint_as_float(c[i].w[k])));
+        return m;
+    } else {                                 // two bf16 at a time
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(c[i].w[k] & 0x7FFF7FFFu));
+        return max_nan(bf16_lo(m), bf16_hi(m));
+    }
+}
+
+template <bool F32, int N>
+__device__ __forceinline__ float chunks_finite_top(const Chunk<F32> (&c)[N]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float f[8];
+        chunk_values<F32>(c[i], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, finite_abs(f[k]));
+    }
+    return m;
+}
+
+__device__ __forceinline__ float halfwarp_max_nan(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ bool is_finite(float a) { return a < __int_as_float(0x7F800000); }   // a >= 0 or NaN
+
+// Codes of a chunk. FINITE: it has no other values.
+template <bool F32, bool FINITE>
+__device__ __forceinline__ uint2 chunk_codes(const Chunk<F32>& c, float inv) {
+    float f[8];
+    chunk_values<F32>(c, f);
+    if constexpr (FINITE) {
+        uint32_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = e4m3x2_from_f32(f[2 * k] * inv, f[2 * k + 1] * inv);
+        return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    } else {
+        return encode8(f, inv);
+    }
+}
+
 template <bool F32>
 __device__ __forceinline__ float load_one(const void* x, int64_t i) {
     if constexpr (F32) return __ldg((const float*)x + i);
@@ -75,14 +138,14 @@ __global__ void __launch_bounds__(TPB)
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float f[8], m = 0.0f;
-            chunk_values<F32>(v[u], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(f[i]));
-            const int b = scale_byte(halfwarp_max(m));
             const int64_t c = c0 + 32 * u;
+            float top = halfwarp_max_nan(chunks_top<F32, 1>({v[u]}));
+            const bool finite = __all_sync(0xffffffffu, is_finite(top));
+            if (!finite) top = halfwarp_max(chunks_finite_top<F32, 1>({v[u]}));
+            const int b = scale_byte(top);
+            const float inv = inverse_scale(b);
             if (c < cpr) {
-                codes[r * cpr + c] = encode8(f, inverse_scale(b));
+                codes[r * cpr + c] = finite ? chunk_codes<F32, true>(v[u], inv) : chunk_codes<F32, false>(v[u], inv);
                 if ((lane & 15) == 0) scales[r * nb + (c >> 4)] = (uint8_t)b;
             }
         }
@@ -115,56 +178,57 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- weights: blocks of 128 x 128
 
-// The largest of the block's threads (256).
+// The largest of the block's WARPS warps, of values at least 0; a NaN wins.
+template <int WARPS>
 __device__ __forceinline__ float block_max(float m, float* shared) {
-    m = warp_max(m);
+    m = halfwarp_max_nan(m);
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = m;
     __syncthreads();
     m = shared[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, shared[i]);
+    for (int i = 1; i < WARPS; ++i) m = max_nan(m, shared[i]);
     __syncthreads();                         // shared may be written again
     return m;
 }
 
-// A block of threads per 128 x 128 tile, which stays in registers between the maximum and the codes: 8 elements of 8 rows a
-// thread (D % 8 == 0).
+// A block of threads per 128 x 128 tile, which stays in registers between the maximum and the codes: 8 elements of 8 rows (bf16)
+// or 4 (fp32) a thread (D % 8 == 0).
 template <bool F32>
-__global__ void __launch_bounds__(256)
+constexpr int TILE_ROWS = F32 ? 4 : 8;
+template <bool F32>
+constexpr int TILE_TPB = 2048 / TILE_ROWS<F32>;
+
+template <bool F32>
+__global__ void __launch_bounds__(TILE_TPB<F32>, F32 ? 2 : 3)
     quant_tiles_kernel(const Chunk<F32>* __restrict__ x, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                        int64_t tiles, int64_t R, int64_t cpr, int64_t rb, int64_t nb) {
-    __shared__ float shared[8];
+    constexpr int N = TILE_ROWS<F32>, ROWS = 128 / N, WARPS = TILE_TPB<F32> / 32;
+    __shared__ float shared[WARPS];
     const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t er = t / nb, e = er / rb;
         const int64_t c = (t - er * nb) * 16 + col, r0 = (er - e * rb) * QBLOCK + row;
         const int64_t at = (e * R + r0) * cpr + c;
-        Chunk<F32> v[8];
-        float m = 0.0f;
+        Chunk<F32> v[N];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c < cpr && r0 + 16 * i < R) {
-                v[i] = ld_stream<F32 ? 8 : 4, true>(x + at + 16 * i * cpr);
+        for (int i = 0; i < N; ++i) {
+            if (c < cpr && r0 + ROWS * i < R) {
+                v[i] = ld_stream<F32 ? 8 : 4, true>(x + at + ROWS * i * cpr);
             } else {
 #pragma unroll
                 for (int k = 0; k < (F32 ? 8 : 4); ++k) v[i].w[k] = 0u;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f[8];
-            chunk_values<F32>(v[i], f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, finite_abs(f[k]));
-        }
-        const int b = scale_byte(block_max(m, shared));
+        float top = block_max<WARPS>(chunks_top<F32>(v), shared);
+        const bool finite = is_finite(top);  // the same for all threads
+        if (!finite) top = block_max<WARPS>(chunks_finite_top<F32>(v), shared);
+        const int b = scale_byte(top);
         const float inv = inverse_scale(b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f[8];
-            chunk_values<F32>(v[i], f);
-            if (c < cpr && r0 + 16 * i < R) codes[at + 16 * i * cpr] = encode8(f, inv);
-        }
+        for (int i = 0; i < N; ++i)
+            if (c < cpr && r0 + ROWS * i < R)
+                codes[at + ROWS * i * cpr] = finite ? chunk_codes<F32, true>(v[i], inv) : chunk_codes<F32, false>(v[i], inv);
         if (threadIdx.x == 0) scales[t] = (uint8_t)b;
     }
 }
@@ -182,7 +246,7 @@ __global__ void __launch_bounds__(256)
         float m = 0.0f;
         if (c < D)
             for (int64_t r = r0 + (threadIdx.x >> 7); r < r1; r += 2) m = fmaxf(m, finite_abs(load_one<F32>(x, (e * R + r) * D + c)));
-        const int b = scale_byte(block_max(m, shared));
+        const int b = scale_byte(block_max<8>(m, shared));
         const float inv = inverse_scale(b);
         if (c < D)
             for (int64_t r = r0 + (threadIdx.x >> 7); r < r1; r += 2) {
@@ -196,8 +260,8 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------- back
 
 // 8 codes a lane (D % 8 == 0), rows and weights alike: the scale of element (e, r, d) is
-// scales[(e·rb + r / block_rows)·nb + d / 128].
-template <bool F32>
+// scales[(e·rb + r / block_rows)·nb + d / 128]. FLAT: rows whose D is a multiple of 128, so chunk i has scale i / 16.
+template <bool F32, bool FLAT>
 __global__ void __launch_bounds__(256)
     dequant_kernel(const uint2* __restrict__ codes, const uint8_t* __restrict__ scales, Chunk<F32>* __restrict__ x,
                    int64_t chunks, int64_t R, int64_t cpr, int64_t rb, int64_t nb, int block_shift) {
@@ -211,13 +275,17 @@ __global__ void __launch_bounds__(256)
             const int64_t i = i0 + u * step;
             if (i < chunks) {
                 asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(q[u].x), "=r"(q[u].y) : "l"(codes + i));
-                const int64_t er = i / cpr, c = i - er * cpr;
-                int64_t at = er;             // the scales' row
-                if (block_shift) {
-                    const int64_t e = er / R;
-                    at = e * rb + ((er - e * R) >> block_shift);
+                int64_t at = i >> 4;
+                if constexpr (!FLAT) {
+                    const int64_t er = i / cpr, c = i - er * cpr;
+                    at = er;                 // the scales' row
+                    if (block_shift) {
+                        const int64_t e = er / R;
+                        at = e * rb + ((er - e * R) >> block_shift);
+                    }
+                    at = at * nb + (c >> 4);
                 }
-                s[u] = scale_value(__ldg(scales + at * nb + (c >> 4)));
+                s[u] = scale_value(__ldg(scales + at));
             }
         }
 #pragma unroll
@@ -283,7 +351,7 @@ int launch_quant(const void* x, uint8_t* codes, uint8_t* scales, int64_t E, int6
     }
     const int64_t rb = (R + QBLOCK - 1) / QBLOCK, tiles = E * rb * nb;
     if (!vec) return launch(quant_tiles_any_kernel<F32>, 256, tiles * 8, stream, x, codes, scales, tiles, R, D, rb, nb);
-    return launch(quant_tiles_kernel<F32>, 256, tiles * 8, stream, (const Chunk<F32>*)x, (uint2*)codes, scales, tiles, R,
+    return launch(quant_tiles_kernel<F32>, TILE_TPB<F32>, tiles * (TILE_TPB<F32> / 32), stream, (const Chunk<F32>*)x, (uint2*)codes, scales, tiles, R,
                   D / 8, rb, nb);
 }
 
@@ -294,7 +362,7 @@ int launch_dequant(const uint8_t* codes, const uint8_t* scales, void* x, int64_t
     const int shift = block_rows == 1 ? 0 : 7;
     if (D % 8 == 0 && aligned(x, F32 ? 32 : 16) && aligned(codes, 8)) {
         const int64_t chunks = E * R * (D / 8);
-        return launch(dequant_kernel<F32>, 256, (chunks + 31) / 32, stream, (const uint2*)codes, scales, (Chunk<F32>*)x,
+        return launch(block_rows == 1 && D % QBLOCK == 0 ? dequant_kernel<F32, true> : dequant_kernel<F32, false>, 256, (chunks + 31) / 32, stream, (const uint2*)codes, scales, (Chunk<F32>*)x,
                       chunks, R, D / 8, rb, nb, shift);
     }
     return launch(dequant_any_kernel<F32>, 256, (E * R * D + 31) / 32, stream, codes, scales, x, E * R * D, R, D, rb, nb,
