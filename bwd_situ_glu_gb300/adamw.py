@@ -12,6 +12,7 @@ mean kept. The conventions are those of the module ``moe``.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import numpy as np
 import torch
@@ -20,7 +21,9 @@ import bwd_situ_glu_gb300 as _sg
 from bwd_situ_glu_gb300 import AdamParams, _check, load as _lib
 from bwd_situ_glu_gb300.moe import _device_now, _elsewhere, _ptr, _raw_stream, _CODE, _F32, _BF16
 
-_U8 = torch.uint8
+_T, _U8 = torch.Tensor, torch.uint8
+_TYPES = {torch.Tensor, torch.nn.Parameter}
+_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
 _E4M3 = 2         # SITU_E4M3
 _COEFFICIENTS = 9  # words of situ_adamw_coefficients
 
@@ -57,7 +60,8 @@ class AdamWPlan:
 
     ``params``: fp32 tensors of any shape; ``m``, ``v``: fp32 of the same shapes, or uint8 codes with ``m_scales`` and
     ``v_scales`` (uint8, ceil(n / 128) each); ``work``: bf16 of the same shapes, or None. All contiguous, on one CUDA device, and
-    no two sharing memory. The plan holds them; ``step`` updates them in place."""
+    no two sharing memory. The plan holds them; ``step`` updates them in place. A parameter's or working copy's ``.data`` may be
+    replaced between steps by one of the same kind; states are refilled with copy_ (a plan whose states were moved raises)."""
 
     def __init__(self, params, m, v, m_scales=None, v_scales=None, work=None):
         params, m, v = list(params), list(m), list(v)
@@ -89,6 +93,14 @@ class AdamWPlan:
             if name in lists:
                 self._table[:, column] = [t.data_ptr() for t in lists[name]]
         self._table[:, 7] = [p.numel() for p in params]
+        self._states = {name: [t.data_ptr() for t in ts] for name, ts in lists.items() if name not in ("params", "work")}
+
+    def _alike(self, tensors, dtype):
+        """Whether every one is contiguous, of this type, of its parameter's shape and on the plan's device. One pass of map for each
+        property takes half the time of one loop with all of them (64 tensors: 75 us of host time a step, now 50)."""
+        return ((set(map(type, tensors)) <= _TYPES or all([isinstance(t, _T) for t in tensors]))
+                and set(map(_dtype, tensors)) == {dtype} and set(map(_T.get_device, tensors)) == {self._device.index}
+                and all(map(_T.is_contiguous, tensors)) and list(map(_shape, tensors)) == self._shapes)
 
     def step(self, grads, params, seed=None, grad_scale=None, stream=None):
         """One step with ``grads`` (a tensor for each parameter, all fp32 or all bf16) and ``params``: adam_params(...), or an int32
@@ -115,25 +127,26 @@ class AdamWPlan:
         kind = grads[0].dtype if isinstance(grads[0], torch.Tensor) else None
         if kind not in _CODE:
             raise TypeError(f"grads must be torch.float32 or torch.bfloat16 tensors, got {kind}")
-        # a parameter's .data may have been replaced since: checked like the gradients, each time. (One pass of a list per
-        # property takes half the time of one pass with all of them: 64 tensors 75 -> 50 us a step.)
-        at, ps = dev.index, self._params
-        if not (all([isinstance(g, torch.Tensor) for g in grads]) and [g.shape for g in grads] == self._shapes
-                and all([g.dtype is kind for g in grads]) and all([g.get_device() == at for g in grads])
-                and all([g.is_contiguous() for g in grads])):
+        if not self._alike(grads, kind):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):
                 _sg._need(g, kind, shape, f"grads[{i}]")
             raise ValueError("all tensors must be on the same device")
-        if not ([p.shape for p in ps] == self._shapes and all([p.dtype is _F32 for p in ps])
-                and all([p.get_device() == at for p in ps]) and all([p.is_contiguous() for p in ps])):
-            for i, (p, shape) in enumerate(zip(ps, self._shapes)):
-                _sg._need(p, _F32, shape, f"params[{i}]")
-            raise ValueError("all tensors must be on the same device")
+        for name, want in (("params", _F32), ("work", _BF16)):
+            held = self._lists.get(name)
+            if held is not None and not self._alike(held, want):
+                for i, (p, shape) in enumerate(zip(held, self._shapes)):
+                    _sg._need(p, want, shape, f"{name}[{i}]")
+                raise ValueError("all tensors must be on the same device")
         if stream is not None or dev.index != _device_now():
             return _elsewhere(stream, self._params[0], lambda: self.step(grads, params, seed, grad_scale))
+        for name, at in self._states.items():
+            if list(map(_T.data_ptr, self._lists[name])) != at:
+                raise ValueError(f"{name} is no longer where it was when the plan was made: make another plan")
         table = self._table
-        table[:, 0] = [p.data_ptr() for p in ps]
-        table[:, 1] = [g.data_ptr() for g in grads]
+        table[:, 0] = list(map(_T.data_ptr, self._params))
+        if "work" in self._lists:
+            table[:, 6] = list(map(_T.data_ptr, self._lists["work"]))
+        table[:, 1] = list(map(_T.data_ptr, grads))
         if not on_device and seed is None:
             seed = params.step
         _check(_lib().situ_adamw_step(table.ctypes.data, len(table), _CODE[kind], _E4M3 if self._eight else _CODE[_F32],

@@ -255,63 +255,71 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // ------------------------------------------------ scales (both CTAs): lane l has rows l, l + 32, .. of the chunk
         int group = 0;
         uint32_t phase = 0;
-        bool ok = true;
         const bool words = KB % 4 == 0 && (uintptr_t)row_scales % 4 == 0;
-        for (int j = j0; ok && j < jobs; j += jstep) {
-            const Job q = job_at(j, plan, E, NT);
+        // A group's bytes, as loaded (a word of a row, or its bytes apart), a group ahead over the jobs: they are not touched before
+        // the next turn, which would wait for them here. 127 (a factor of 1) where there is nothing.
+        uint32_t raw_w[GROUP_KB], raw[7][GROUP_KB];
+        auto fetch = [&](const Job& q, int kb) {
             const int cb = q.nt * 2 + rank;                      // this CTA's block of output columns
-            const uint8_t* wp = w_scales + q.e * ws.per_expert + (int64_t)cb * ws.col_step;
-            const uint8_t* rp = row_scales + (int64_t)(q.row0 + lane) * KB;
-            // A group's bytes, as loaded (a word of a row, or its bytes apart), a group ahead: they are not touched before the next
-            // turn, which would wait for them here. 127 (a factor of 1) where there is nothing.
-            uint32_t raw_w[GROUP_KB], raw[7][GROUP_KB];
-            auto fetch = [&](int kb) {
+            const uint8_t* wp = w_scales + q.e * ws.per_expert + (int64_t)cb * ws.col_step + (int64_t)kb * ws.k_step;
+            const uint8_t* rp = row_scales + (int64_t)(q.row0 + lane) * KB + kb;
 #pragma unroll
-                for (int k = 0; k < GROUP_KB; ++k) {
-                    raw_w[k] = 127u;
-                    if (cb < ws.col_blocks && kb + k < KB) raw_w[k] = __ldg(wp + (int64_t)(kb + k) * ws.k_step);
-                }
+            for (int k = 0; k < GROUP_KB; ++k) {
+                raw_w[k] = 127u;
+                if (cb < ws.col_blocks && kb + k < KB) raw_w[k] = __ldg(wp + (int64_t)k * ws.k_step);
+            }
 #pragma unroll
-                for (int i = 0; i < 7; ++i) {
-                    const bool live = lane + 32 * i < q.rows;
-                    const uint8_t* p = rp + (int64_t)(32 * i) * KB + kb;
-                    raw[i][0] = 0x7F7F7F7Fu;
-                    if (words) {
-                        if (live) raw[i][0] = __ldg((const uint32_t*)p);
-                    } else {
+            for (int i = 0; i < 7; ++i) {
+                const bool live = lane + 32 * i < q.rows;
+                const uint8_t* p = rp + (int64_t)(32 * i) * KB;
+                raw[i][0] = 0x7F7F7F7Fu;
+                if (words) {
+                    if (live) raw[i][0] = __ldg((const uint32_t*)p);
+                } else {
 #pragma unroll
-                        for (int k = 0; k < GROUP_KB; ++k) {
-                            raw[i][k] = 127u;
-                            if (live && kb + k < KB) raw[i][k] = __ldg(p + k);
-                        }
+                    for (int k = 0; k < GROUP_KB; ++k) {
+                        raw[i][k] = 127u;
+                        if (live && kb + k < KB) raw[i][k] = __ldg(p + k);
                     }
                 }
-            };
-            fetch(0);
-            for (int kb = 0; kb < KB; kb += GROUP_KB) {
-                uint32_t b[7];
-                const uint32_t wb = bytes4(raw_w[0], raw_w[1], raw_w[2], raw_w[3]);
-#pragma unroll
-                for (int i = 0; i < 7; ++i) b[i] = words ? raw[i][0] : bytes4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]);
-                if (kb + GROUP_KB < KB) fetch(kb + GROUP_KB);
-                if (!pair_wait(&sbars->empty[group], phase ^ 1, &bars->abort, status)) { ok = false; break; }
-                uint8_t* at = scales + group * GROUP_KB * SCALE_BYTES + lane * 16;
-#pragma unroll
-                for (int k = 0; k < GROUP_KB; ++k) {
-                    if (kb + k >= KB) break;
-                    uint32_t v[7];
-#pragma unroll
-                    for (int i = 0; i < 7; ++i) v[i] = __byte_perm(b[i], 0, k * 0x1111);
-                    const uint32_t w = __byte_perm(wb, 0, k * 0x1111);
-                    st_shared_v4(at + k * SCALE_BYTES, w, w, w, w);
-                    st_shared_v4(at + k * SCALE_BYTES + SCALE_PIECE, v[0], v[1], v[2], v[3]);
-                    st_shared_v4(at + k * SCALE_BYTES + 2 * SCALE_PIECE, v[4], v[5], v[6], 0x7F7F7F7Fu);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&sbars->full[group], 0));
-                if (++group == GROUPS) { group = 0; phase ^= 1; }
             }
+        };
+        int j = j0, kb = 0;
+        Job next = {};
+        if (j < jobs) {
+            next = job_at(j, plan, E, NT);
+            fetch(next, 0);
+        }
+        while (j < jobs) {
+            const int blocks = min(GROUP_KB, KB - kb);
+            uint32_t b[7];
+            const uint32_t wb = bytes4(raw_w[0], raw_w[1], raw_w[2], raw_w[3]);
+#pragma unroll
+            for (int i = 0; i < 7; ++i) b[i] = words ? raw[i][0] : bytes4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]);
+            kb += GROUP_KB;
+            if (kb >= KB) {
+                kb = 0;
+                j += jstep;
+                if (j < jobs) next = job_at(j, plan, E, NT);
+            }
+            if (j < jobs) fetch(next, kb);
+            if (!pair_wait(&sbars->empty[group], phase ^ 1, &bars->abort, status)) break;
+            uint8_t* at = scales + group * GROUP_KB * SCALE_BYTES + lane * 16;
+#pragma unroll
+            for (int k = 0; k < GROUP_KB; ++k) {
+                if (k >= blocks) break;
+                uint32_t v[7];
+#pragma unroll
+                for (int i = 0; i < 7; ++i) v[i] = __byte_perm(b[i], 0, k * 0x1111);
+                const uint32_t w = __byte_perm(wb, 0, k * 0x1111);
+                st_shared_v4(at + k * SCALE_BYTES, w, w, w, w);
+                st_shared_v4(at + k * SCALE_BYTES + SCALE_PIECE, v[0], v[1], v[2], v[3]);
+                st_shared_v4(at + k * SCALE_BYTES + 2 * SCALE_PIECE, v[4], v[5], v[6], 0x7F7F7F7Fu);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&sbars->full[group], 0));
+            if (++group == GROUPS) { group = 0; phase ^= 1; }
         }
     } else {
         linear_epilogue<ACT>(bars, plan, tmem, ACC_COLS, patches, bias, residual, out, out_fp32, pre, status, E, NCOL, NT, j0,

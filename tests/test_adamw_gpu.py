@@ -355,6 +355,16 @@ def test_another_stream_and_replaced_data():
     plan.step(t["grads"], hp, stream=s)
     s.synchronize()
     assert torch.equal(t["params"][0], u["params"][0]) and torch.equal(t["m"][0], u["m"][0])
+    t["work"][0].data = torch.zeros_like(t["work"][0])
+    for x, y in ((t, plan), (u, plan_of(u))):
+        y.step(x["grads"], sg.adam_params(step=10, **HP))
+    assert torch.equal(t["work"][0], u["work"][0])
+    t["v"][0].data = t["v"][0].data.clone()
+    with pytest.raises(ValueError):
+        plan.step(t["grads"], hp)
+    t["params"][0].data = t["params"][0].data[:69999].clone()
+    with pytest.raises(ValueError):
+        plan.step(t["grads"], hp)
 
 
 def test_elements_past_32_bits():
