@@ -42,17 +42,17 @@ constexpr int KB8 = 128;                     // elements (bytes) of the contract
 constexpr int UK8 = 32;                      // elements per tcgen05.mma
 constexpr int MAX_CHUNK = 224;               // rows per job
 constexpr int ACC_COLS = 224;                // TMEM columns of an accumulator
-constexpr int SCALE_WARP = 2 + NUM_EPI_WARPS;
-constexpr int NUM_THREADS = (SCALE_WARP + 1) * 32;    // TMA, MMA, epilogue, scales
+constexpr int SCALE_WARP = 2 + NUM_EPI_WARPS, SCALE_WARPS = 2;
+constexpr int NUM_THREADS = (SCALE_WARP + SCALE_WARPS) * 32;    // TMA, MMA, epilogue, scales
 
 // Scale bytes of a stage in shared memory: 128 rows are 512 bytes, row i at 16·(i % 32) + 4·(i / 32), as tcgen05.cp
 // 32x128b takes them. One such piece for the weights, two for the rows.
 constexpr int SCALE_PIECE = 512;
 constexpr int SCALE_BYTES = 3 * SCALE_PIECE;
 constexpr int SCALE_COL0 = 2 * ACC_COLS;     // in TMEM: 4 columns a piece
-constexpr int SCALE_SLOTS = 5;               // blocks whose scales TMEM holds; the tensor core takes copies and MMAs in order
-constexpr int GROUP_KB = 4, GROUPS = 2;      // blocks whose scales are handed over at once; such groups in shared memory
-static_assert(SCALE_COL0 + SCALE_SLOTS * 12 <= TMEM_COLS, "TMEM columns");
+constexpr int GROUP_KB = 4, GROUPS = SCALE_WARPS;   // blocks whose scales are handed over at once; such groups in shared memory
+// TMEM holds the scales of GROUP_KB blocks; the tensor core takes copies and MMAs of one thread in order
+static_assert(SCALE_COL0 + GROUP_KB * 12 <= TMEM_COLS, "TMEM columns");
 
 // A ring stage: 128 weight rows and half of the chunk's rows, 128 bytes each.
 __host__ __device__ constexpr int stage_bytes(int most) { return PA_BYTES + most / 2 * KB8; }
@@ -65,6 +65,7 @@ __host__ __device__ constexpr int ring_stages(int most) {
 struct alignas(8) ScaleBars {
     uint64_t full[GROUPS];                   // leader's: both CTAs have written a group
     uint64_t empty[GROUPS];                  // both: the commit of the MMAs behind a group's copies
+    int rows[GROUPS];                        // leader's: the MMA's N of a group's job
 };
 
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + GROUPS * GROUP_KB * SCALE_BYTES + NUM_EPI_WARPS * PATCH + (int)sizeof(PairBars) + (int)sizeof(ScaleBars) +
@@ -188,76 +189,68 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (rank == 0) pair_drain(bars, pending, pend_par);
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader; the warp converged, one lane issues)
+        // What this warp executes for a block is dependent instructions of one thread, and has to take less time than the
+        // block's products (448 cycles for 224 rows): four blocks at a time with their offsets as constants, and a job's size
+        // from the scale warp. (With the scales' bookkeeping block by block and the work list searched here, a block took 670
+        // cycles with 64 rows and 750 with 224; 16385 x 3584 x 3584 160 us.)
         if (rank == 0) {
             const bool elected = elect_one();
-            int stage = 0, job = 0, slot = 0;
-            uint32_t phase = 0;
+            int stage = 0, job = 0, group = 0;
+            uint32_t phase = 0, gphase = 0;
             bool ok = true;
-            int n_next = j0 < jobs ? job_at(j0, plan, E, NT).n : 0;
-            const uint32_t ring_addr = smem_addr(ring), scale_addr = smem_addr(scales);
-            // The scales of the block after the one that was copied last, over the jobs: one block ahead of the products, which
-            // otherwise wait for each copy.
-            int cj = j0, ckb = 0, cslot = 0, group = 0;
-            uint32_t gphase = 0;
-            auto copy_next = [&]() {
-                if (cj >= jobs) return true;
-                const int k = ckb % GROUP_KB;
-                if (k == 0) {
-                    if (!pair_wait<true>(&sbars->full[group], gphase, &bars->abort, status)) return false;
-                    tc_fence_after();
-                }
-                const bool end = ckb + 1 == KB, last = end || k == GROUP_KB - 1;     // of the job, of the group
-                if (elected) {
-                    const uint64_t sd = scale_desc(scale_addr + (uint32_t)((group * GROUP_KB + k) * SCALE_BYTES));
-                    const uint32_t at = tmem + (uint32_t)(SCALE_COL0 + cslot * 12);
-                    copy_scales(at, sd);
-                    copy_scales(at + 4, sd + (SCALE_PIECE >> 4));
-                    copy_scales(at + 8, sd + 2 * (SCALE_PIECE >> 4));
-                    if (last) pair_commit(&sbars->empty[group]);
-                }
-                if (last && ++group == GROUPS) { group = 0; gphase ^= 1; }
-                if (++cslot == SCALE_SLOTS) cslot = 0;
-                ++ckb;
-                if (end) { ckb = 0; cj += jstep; }
-                return true;
-            };
-            ok = copy_next();
+            const uint32_t ring_addr = smem_addr(ring);
+            const uint64_t sd0 = scale_desc(smem_addr(scales));
+            const uint32_t sf = tmem + (uint32_t)SCALE_COL0;
             for (int j = j0; ok && j < jobs; j += jstep, ++job) {
-                const uint32_t idesc = scaled_idesc(n_next, W_MN);
+                uint32_t idesc = 0;
+                int pieces = 3;                                  // of scales: the weights', and one or two of the rows'
                 const int acc = job & 1;
                 const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
                 if (!pair_wait<true>(&bars->tempty[acc], (uint32_t)((job >> 1) & 1) ^ 1, &bars->abort, status)) break;
-                tc_fence_after();
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!pair_wait(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t sa = ring_addr + (uint32_t)(stage * sbytes);
-                    const uint64_t ad = W_MN ? smem_desc_mn8(sa) : smem_desc(sa), bd = smem_desc(sa + PA_BYTES);
-                    const uint32_t sft = tmem + (uint32_t)(SCALE_COL0 + slot * 12);
-                    if (elected) scaled_mma(d, ad, bd, idesc, sft, sft + 4, (uint32_t)kb);
-                    if (!copy_next()) { ok = false; break; }
-                    if (elected) {
-#pragma unroll
-                        for (int kk = 1; kk < KB8 / UK8; ++kk)   // 32 deep: 32 bytes along a row, 4096 bytes MN-major
-                            scaled_mma(d, ad + (uint64_t)(kk * (W_MN ? 256 : 2)), bd + (uint64_t)(kk * 2), idesc, sft, sft + 4, 1u);
-                        pair_commit(&bars->empty[stage]);
+                for (int kb0 = 0; ok && kb0 < KB; kb0 += GROUP_KB) {
+                    if (!pair_wait<true>(&sbars->full[group], gphase, &bars->abort, status)) { ok = false; break; }
+                    if (kb0 == 0) {
+                        const int n = *(volatile int*)&sbars->rows[group];
+                        idesc = scaled_idesc(n, W_MN);
+                        pieces = n > 128 ? 3 : 2;
                     }
-                    if (++stage == stages) { stage = 0; phase ^= 1; }
-                    if (++slot == SCALE_SLOTS) slot = 0;
-                    if (kb == 0 && j + jstep < jobs) n_next = job_at(j + jstep, plan, E, NT).n;   // while these run
+                    const uint64_t sd = sd0 + (uint64_t)(group * (GROUP_KB * SCALE_BYTES >> 4));
+#pragma unroll
+                    for (int k = 0; k < GROUP_KB; ++k) {
+                        if (kb0 + k >= KB) break;
+                        if (!pair_wait(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t sa = ring_addr + (uint32_t)(stage * sbytes);
+                        const uint64_t ad = W_MN ? smem_desc_mn8(sa) : smem_desc(sa), bd = smem_desc(sa + PA_BYTES);
+                        if (elected) {
+#pragma unroll
+                            for (int i = 0; i < 3; ++i)
+                                if (i < pieces) copy_scales(sf + k * 12 + i * 4, sd + (uint64_t)((k * SCALE_BYTES + i * SCALE_PIECE) >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < KB8 / UK8; ++kk)   // 32 deep: 32 bytes along a row, 4096 bytes MN-major
+                                scaled_mma(d, ad + (uint64_t)(kk * (W_MN ? 256 : 2)), bd + (uint64_t)(kk * 2), idesc, sf + k * 12,
+                                           sf + k * 12 + 4, kk > 0 || k > 0 ? 1u : (uint32_t)kb0);
+                            pair_commit(&bars->empty[stage]);
+                        }
+                        if (++stage == stages) { stage = 0; phase ^= 1; }
+                    }
+                    if (ok && elected) pair_commit(&sbars->empty[group]);
+                    if (++group == GROUPS) { group = 0; gphase ^= 1; }
                 }
                 if (ok && elected) pair_commit(&bars->tfull[acc]);
             }
             __syncwarp();
             if (elected) pair_commit(&bars->mma_done);
         }
-    } else if (warp == SCALE_WARP) {
+    } else if (warp >= SCALE_WARP) {
         // ------------------------------------------------ scales (both CTAs): lane l has rows l, l + 32, .. of the chunk
-        int group = 0;
+        // Each of the warps takes every SCALE_WARPS-th group of the pair's jobs, into a buffer of its own: some 300 dependent
+        // instructions, which took one warp longer than the products of the group's four blocks.
+        const int group = warp - SCALE_WARP, NG = (KB + GROUP_KB - 1) / GROUP_KB;
         uint32_t phase = 0;
         const bool words = KB % 4 == 0 && (uintptr_t)row_scales % 4 == 0;
-        // A group's bytes, as loaded (a word of a row, or its bytes apart), a group ahead over the jobs: they are not touched before
-        // the next turn, which would wait for them here. 127 (a factor of 1) where there is nothing.
+        // A group's bytes, as loaded (a word of a row, or its bytes apart), a turn ahead: they are not touched before the next
+        // turn, which would wait for them here. 127 (a factor of 1) where there is nothing.
         uint32_t raw_w[GROUP_KB], raw[7][GROUP_KB];
         auto fetch = [&](const Job& q, int kb) {
             const int cb = q.nt * 2 + rank;                      // this CTA's block of output columns
@@ -284,26 +277,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
         };
-        int j = j0, kb = 0;
+        int j = j0, g = group;                                   // the next group: its job, and which of the job's
         Job next = {};
-        if (j < jobs) {
-            next = job_at(j, plan, E, NT);
-            fetch(next, 0);
-        }
+        auto settle = [&](bool moved) {                          // g may have run past its job's last
+            while (g >= NG) {
+                g -= NG;
+                j += jstep;
+                moved = true;
+            }
+            if (moved && j < jobs) next = job_at(j, plan, E, NT);
+        };
+        settle(true);
+        if (j < jobs) fetch(next, g * GROUP_KB);
         while (j < jobs) {
-            const int blocks = min(GROUP_KB, KB - kb);
+            const int blocks = min(GROUP_KB, KB - g * GROUP_KB), rows = next.n;
             uint32_t b[7];
             const uint32_t wb = bytes4(raw_w[0], raw_w[1], raw_w[2], raw_w[3]);
 #pragma unroll
             for (int i = 0; i < 7; ++i) b[i] = words ? raw[i][0] : bytes4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]);
-            kb += GROUP_KB;
-            if (kb >= KB) {
-                kb = 0;
-                j += jstep;
-                if (j < jobs) next = job_at(j, plan, E, NT);
-            }
-            if (j < jobs) fetch(next, kb);
+            g += SCALE_WARPS;
+            settle(false);
+            if (j < jobs) fetch(next, g * GROUP_KB);
             if (!pair_wait(&sbars->empty[group], phase ^ 1, &bars->abort, status)) break;
+            if (lane == 0) sbars->rows[group] = rows;
             uint8_t* at = scales + group * GROUP_KB * SCALE_BYTES + lane * 16;
 #pragma unroll
             for (int k = 0; k < GROUP_KB; ++k) {
@@ -314,12 +310,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t w = __byte_perm(wb, 0, k * 0x1111);
                 st_shared_v4(at + k * SCALE_BYTES, w, w, w, w);
                 st_shared_v4(at + k * SCALE_BYTES + SCALE_PIECE, v[0], v[1], v[2], v[3]);
-                st_shared_v4(at + k * SCALE_BYTES + 2 * SCALE_PIECE, v[4], v[5], v[6], 0x7F7F7F7Fu);
+                if (rows > 128) st_shared_v4(at + k * SCALE_BYTES + 2 * SCALE_PIECE, v[4], v[5], v[6], 0x7F7F7F7Fu);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(cluster_addr(&sbars->full[group], 0));
-            if (++group == GROUPS) { group = 0; phase ^= 1; }
+            phase ^= 1;
         }
     } else {
         linear_epilogue<ACT>(bars, plan, tmem, ACC_COLS, patches, bias, residual, out, out_fp32, pre, status, E, NCOL, NT, j0,
