@@ -106,8 +106,10 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
     return a | (b << 8) | (c << 16) | (d << 24);
 }
 
+// A CTA's half of a chunk's rows is a multiple of 16: a map, and so one load a stage, for each (boxes of 16 (i + 1) rows).
+constexpr int ROW_MAPS = MAX_CHUNK / 32;
 struct RowMaps {
-    CUtensorMap m[4];                        // boxes of 128 >> i rows
+    CUtensorMap m[ROW_MAPS];
 };
 
 // Where a weight's scale bytes are: expert e's block of output columns c and block kb of the contraction at
@@ -154,30 +156,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int stage = 0;
         uint32_t phase = 0, pending = 0, pend_par = 0;
         const uint64_t pol_w = make_policy<kHintB>(), pol_r = make_policy<kHintA>();
+        const uint32_t full0 = cluster_addr(&bars->full[0], 0);
         bool ok = true;
         Job next = {};
         if (j0 < jobs) next = job_at(j0, plan, E, NT);
         for (int j = j0; ok && j < jobs; j += jstep) {
             const Job q = next;
-            const int c0 = q.nt * TILE + rank * 128;
+            const int c0 = q.nt * TILE + rank * 128, r0 = q.row0 + rank * (q.n >> 1);
             const uint32_t bytes = (uint32_t)(2 * PA_BYTES + q.n * KB8);
+            const CUtensorMap* map_rows = &map_r.m[(q.n >> 5) - 1];
             for (int kb = 0; kb < KB; ++kb) {
                 if (!pair_wait(&bars->empty[stage], phase ^ 1, &bars->abort, status)) { ok = false; break; }
                 if (elected) {
                     if (rank == 0) mbar_expect_tx(&bars->full[stage], bytes);
-                    const uint32_t bar = cluster_addr(&bars->full[stage], 0);
+                    const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
                     uint8_t* sa = ring + stage * sbytes;
                     if constexpr (W_MN) pair_load_3d(sa, &map_w, c0, kb * KB8, q.e, bar, pol_w);
                     else pair_load_3d(sa, &map_w, kb * KB8, c0, q.e, bar, pol_w);
-                    const int half = q.n >> 1;                   // rows of this CTA: a multiple of 16
-                    int at = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (half & (128 >> i)) {
-                            pair_load_2d(sa + PA_BYTES + at * KB8, &map_r.m[i], kb * KB8, q.row0 + rank * half + at, bar, pol_r);
-                            at += 128 >> i;
-                        }
-                    }
+                    pair_load_2d(sa + PA_BYTES, map_rows, kb * KB8, r0, bar, pol_r);
                 }
                 pending |= 1u << stage;
                 pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
@@ -514,8 +510,8 @@ int launch_tc(const Args& p) {
     CUtensorMap map_w;
     RowMaps map_r;
     const uint64_t rdims[2] = {(uint64_t)KC, (uint64_t)p.R}, rstride[1] = {(uint64_t)KC};
-    for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t box[2] = {KB8, 128u >> i};
+    for (uint32_t i = 0; i < ROW_MAPS; ++i) {
+        const uint32_t box[2] = {KB8, 16 * (i + 1)};
         if (!make_map_bytes(&map_r.m[i], p.a, 2, rdims, rstride, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
             return cuda_fail(cudaErrorInvalidValue);
     }
