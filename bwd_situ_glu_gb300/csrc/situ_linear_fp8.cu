@@ -38,7 +38,7 @@ using namespace situ_linear;
 using namespace situ_linear_tc;
 using namespace situ_fp8;
 
-constexpr int KB8 = 128;                     // elements (bytes) of the contraction per ring stage: one scale block
+constexpr int KB8 = 128;                     // elements (bytes) of a block of the contraction: one scale
 constexpr int UK8 = 32;                      // elements per tcgen05.mma
 constexpr int MAX_CHUNK = 224;               // rows per job
 constexpr int ACC_COLS = 224;                // TMEM columns of an accumulator
@@ -54,11 +54,14 @@ constexpr int GROUP_KB = 4, GROUPS = SCALE_WARPS;   // blocks whose scales are h
 // TMEM holds the scales of GROUP_KB blocks; the tensor core takes copies and MMAs of one thread in order
 static_assert(SCALE_COL0 + GROUP_KB * 12 <= TMEM_COLS, "TMEM columns");
 
-// A ring stage: 128 weight rows and half of the chunk's rows, 128 bytes each.
-__host__ __device__ constexpr int stage_bytes(int most) { return PA_BYTES + most / 2 * KB8; }
-constexpr int RING_BYTES = 6 * stage_bytes(MAX_CHUNK);
+// A ring stage: two blocks, of each 128 weight rows and half of the chunk's rows, 128 bytes each. (A stage's waits, its loads'
+// announcement and its commit take some 430 cycles however little it holds: with one block a stage 224 rows took 640
+// cycles a block.)
+constexpr int STAGE_KB = 2;
+__host__ __device__ constexpr int block_bytes(int most) { return PA_BYTES + most / 2 * KB8; }
+constexpr int RING_BYTES = 3 * STAGE_KB * block_bytes(MAX_CHUNK);
 __host__ __device__ constexpr int ring_stages(int most) {
-    const int s = RING_BYTES / stage_bytes(most);
+    const int s = RING_BYTES / (STAGE_KB * block_bytes(most));
     return s < PSTAGES ? s : PSTAGES;
 }
 
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int NT = (int)((NCOL + TILE - 1) / TILE);
-    const int sbytes = stage_bytes(most), stages = ring_stages(most);
+    const int bbytes = block_bytes(most), sbytes = STAGE_KB * bbytes, stages = ring_stages(most);
 
     build_plan(plan, offsets, E, R, most);
     if (threadIdx.x == 0) {                  // before pair_setup's fence and barriers
@@ -165,15 +168,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int c0 = q.nt * TILE + rank * 128, r0 = q.row0 + rank * (q.n >> 1);
             const uint32_t bytes = (uint32_t)(2 * PA_BYTES + q.n * KB8);
             const CUtensorMap* map_rows = &map_r.m[(q.n >> 5) - 1];
-            for (int kb = 0; kb < KB; ++kb) {
+            for (int kb = 0; kb < KB; kb += STAGE_KB) {
                 if (!pair_wait(&bars->empty[stage], phase ^ 1, &bars->abort, status)) { ok = false; break; }
                 if (elected) {
-                    if (rank == 0) mbar_expect_tx(&bars->full[stage], bytes);
+                    const int blocks = min(STAGE_KB, KB - kb);
+                    if (rank == 0) mbar_expect_tx(&bars->full[stage], bytes * blocks);
                     const uint32_t bar = full0 + (uint32_t)(stage * sizeof(uint64_t));
                     uint8_t* sa = ring + stage * sbytes;
-                    if constexpr (W_MN) pair_load_3d(sa, &map_w, c0, kb * KB8, q.e, bar, pol_w);
-                    else pair_load_3d(sa, &map_w, kb * KB8, c0, q.e, bar, pol_w);
-                    pair_load_2d(sa + PA_BYTES, map_rows, kb * KB8, r0, bar, pol_r);
+#pragma unroll
+                    for (int i = 0; i < STAGE_KB; ++i) {
+                        if (i >= blocks) break;
+                        const int k = (kb + i) * KB8;
+                        if constexpr (W_MN) pair_load_3d(sa + i * bbytes, &map_w, c0, k, q.e, bar, pol_w);
+                        else pair_load_3d(sa + i * bbytes, &map_w, k, c0, q.e, bar, pol_w);
+                        pair_load_2d(sa + i * bbytes + PA_BYTES, map_rows, k, r0, bar, pol_r);
+                    }
                 }
                 pending |= 1u << stage;
                 pend_par = (pend_par & ~(1u << stage)) | (phase << stage);
@@ -211,26 +220,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         pieces = n > 128 ? 3 : 2;
                     }
                     const uint64_t sd = sd0 + (uint64_t)(group * (GROUP_KB * SCALE_BYTES >> 4));
+                    tc_fence_after();
+                    if (elected) {                               // behind the MMAs of the group before, in the tensor core's order
 #pragma unroll
-                    for (int k = 0; k < GROUP_KB; ++k) {
-                        if (kb0 + k >= KB) break;
-                        if (!pair_wait(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t sa = ring_addr + (uint32_t)(stage * sbytes);
-                        const uint64_t ad = W_MN ? smem_desc_mn8(sa) : smem_desc(sa), bd = smem_desc(sa + PA_BYTES);
-                        if (elected) {
+                        for (int k = 0; k < GROUP_KB; ++k) {
+                            if (kb0 + k >= KB) break;
 #pragma unroll
                             for (int i = 0; i < 3; ++i)
                                 if (i < pieces) copy_scales(sf + k * 12 + i * 4, sd + (uint64_t)((k * SCALE_BYTES + i * SCALE_PIECE) >> 4));
+                        }
+                        pair_commit(&sbars->empty[group]);
+                    }
 #pragma unroll
-                            for (int kk = 0; kk < KB8 / UK8; ++kk)   // 32 deep: 32 bytes along a row, 4096 bytes MN-major
-                                scaled_mma(d, ad + (uint64_t)(kk * (W_MN ? 256 : 2)), bd + (uint64_t)(kk * 2), idesc, sf + k * 12,
-                                           sf + k * 12 + 4, kk > 0 || k > 0 ? 1u : (uint32_t)kb0);
+                    for (int h = 0; h < GROUP_KB; h += STAGE_KB) {
+                        if (kb0 + h >= KB) break;
+                        if (!pair_wait(&bars->full[stage], phase, &bars->abort, status)) { ok = false; break; }
+                        tc_fence_after();
+                        if (elected) {
+#pragma unroll
+                            for (int k = h; k < h + STAGE_KB; ++k) {
+                                if (kb0 + k >= KB) break;
+                                const uint32_t sa = ring_addr + (uint32_t)(stage * sbytes + (k - h) * bbytes);
+                                const uint64_t ad = W_MN ? smem_desc_mn8(sa) : smem_desc(sa), bd = smem_desc(sa + PA_BYTES);
+#pragma unroll
+                                for (int kk = 0; kk < KB8 / UK8; ++kk)   // 32 deep: 32 bytes along a row, 4096 bytes MN-major
+                                    scaled_mma(d, ad + (uint64_t)(kk * (W_MN ? 256 : 2)), bd + (uint64_t)(kk * 2), idesc, sf + k * 12,
+                                               sf + k * 12 + 4, kk > 0 || k > 0 ? 1u : (uint32_t)kb0);
+                            }
                             pair_commit(&bars->empty[stage]);
                         }
                         if (++stage == stages) { stage = 0; phase ^= 1; }
                     }
-                    if (ok && elected) pair_commit(&sbars->empty[group]);
                     if (++group == GROUPS) { group = 0; gphase ^= 1; }
                 }
                 if (ok && elected) pair_commit(&bars->tfull[acc]);
@@ -285,6 +305,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
         settle(true);
         if (j < jobs) fetch(next, g * GROUP_KB);
+        uint8_t* at = scales + group * GROUP_KB * SCALE_BYTES + lane * 16;
+        const uint32_t full = cluster_addr(&sbars->full[group], 0);
         while (j < jobs) {
             const int blocks = min(GROUP_KB, KB - g * GROUP_KB), rows = next.n;
             uint32_t b[7];
@@ -294,23 +316,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             g += SCALE_WARPS;
             settle(false);
             if (j < jobs) fetch(next, g * GROUP_KB);
+            uint32_t v[GROUP_KB][8];                             // before the wait: what follows it delays the products
+#pragma unroll
+            for (int k = 0; k < GROUP_KB; ++k) {
+#pragma unroll
+                for (int i = 0; i < 7; ++i) v[k][i] = __byte_perm(b[i], 0, k * 0x1111);
+                v[k][7] = __byte_perm(wb, 0, k * 0x1111);
+            }
             if (!pair_wait(&sbars->empty[group], phase ^ 1, &bars->abort, status)) break;
             if (lane == 0) sbars->rows[group] = rows;
-            uint8_t* at = scales + group * GROUP_KB * SCALE_BYTES + lane * 16;
 #pragma unroll
             for (int k = 0; k < GROUP_KB; ++k) {
                 if (k >= blocks) break;
-                uint32_t v[7];
-#pragma unroll
-                for (int i = 0; i < 7; ++i) v[i] = __byte_perm(b[i], 0, k * 0x1111);
-                const uint32_t w = __byte_perm(wb, 0, k * 0x1111);
-                st_shared_v4(at + k * SCALE_BYTES, w, w, w, w);
-                st_shared_v4(at + k * SCALE_BYTES + SCALE_PIECE, v[0], v[1], v[2], v[3]);
-                if (rows > 128) st_shared_v4(at + k * SCALE_BYTES + 2 * SCALE_PIECE, v[4], v[5], v[6], 0x7F7F7F7Fu);
+                st_shared_v4(at + k * SCALE_BYTES, v[k][7], v[k][7], v[k][7], v[k][7]);
+                st_shared_v4(at + k * SCALE_BYTES + SCALE_PIECE, v[k][0], v[k][1], v[k][2], v[k][3]);
+                if (rows > 128) st_shared_v4(at + k * SCALE_BYTES + 2 * SCALE_PIECE, v[k][4], v[k][5], v[k][6], 0x7F7F7F7Fu);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&sbars->full[group], 0));
+            if (lane == 0) mbar_arrive_cluster(full);
             phase ^= 1;
         }
     } else {
