@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // loads of weights and of the row at the same place are the fragments of four steps, the contraction's order being
 // free within a block. A block's sum is multiplied by its scales as it is added to the fp32 total.
 constexpr int FEW_WARPS = 8;
-constexpr int FEW_ROWS = 32;                 // rows of one job: 1, 2 or 4 tiles of 8
+constexpr int FEW_ROWS = 16;                 // rows of one job: 1 or 2 tiles of 8
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -485,8 +485,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
         const uint8_t* we = w + (int64_t)lo * N * K;
         const uint8_t* se = ws + ((int64_t)lo * NB + n0 / QBLOCK) * KB;
         if (rows <= 8) few_job<1>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
-        else if (rows <= 16) few_job<2>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
-        else few_job<4>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
+        else few_job<2>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
         __syncthreads();
         for (int i = threadIdx.x; i < rows * 16; i += blockDim.x) {
             const int r = i >> 4, c = i & 15;
@@ -509,9 +508,12 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
 
 // ---------------------------------------------------------------- host side
 
-// Up to how many rows linear_fp8_few_kernel takes the forward: on average two an expert, or 64 in all.
-constexpr int64_t FEW_MAX_MEAN_ROWS = 2;
-constexpr int64_t FEW_MAX_ROWS = 64;
+// What linear_fp8_few_kernel takes of the forward: few rows, and weights that a few SMs' tiles would not stream at HBM's rate.
+// (few / tensor-core kernel, us. One weight of 3584 x 3584: 1 row 6.4 / 11.4, 16 rows 8.6 / 12.1, 32 rows 14.4 / 12.1; of
+// 14336 x 3584: 1 row 13.0 / 16.0. 112 experts of 3584 x 2048: 8 rows 18.2 / 13.9, 128 rows 126 / 83, 448 rows 202 / 128; 8
+// experts of 1024 x 1024: 8 rows 5.2 / 8.3.)
+constexpr int64_t FEW_MAX_ROWS = 16;
+constexpr int64_t FEW_MAX_WEIGHTS = 52 << 20;
 
 struct Args {
     const uint8_t *a, *as, *w, *ws;
@@ -576,7 +578,8 @@ int launch_few(const Args& p) {
 
 template <int ACT>
 int launch_fwd(const Args& p) {
-    return p.R <= FEW_MAX_ROWS || p.R <= p.E * FEW_MAX_MEAN_ROWS ? launch_few<ACT>(p) : launch_tc<false, ACT>(p);
+    const int64_t experts = p.R < p.E ? p.R : p.E;       // with rows, at most
+    return p.R <= FEW_MAX_ROWS && p.N * p.K <= FEW_MAX_WEIGHTS / experts ? launch_few<ACT>(p) : launch_tc<false, ACT>(p);
 }
 
 int check_fp8(int64_t E, const void* offsets, int64_t R, int64_t N, int64_t K) {
