@@ -83,7 +83,7 @@ def situ_dequant_fp8(codes, scales, block_rows=1, dtype=None, out=None, stream=N
 
 def _pair(t, name):
     """(codes, scales) of a quantised tensor."""
-    if not isinstance(t, (tuple, list)) or len(t) != 2 or not all(isinstance(x, torch.Tensor) for x in t):
+    if not isinstance(t, (tuple, list)) or len(t) != 2 or not (isinstance(t[0], torch.Tensor) and isinstance(t[1], torch.Tensor)):
         raise TypeError(f"{name} must be a pair (codes, scales) of situ_quant_fp8")
     return t
 
@@ -181,14 +181,16 @@ def situ_linear_fp8_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, d
                                        _ptr(dbias), _ptr(buf), nb, R, N, s))
     if need_da:
         da = _empty((R, K), dtype=_BF16, device=dev)
-        dq, ds = situ_quant_fp8(dz)
+        dq, ds = _empty((R, N), dtype=_U8, device=dev), _empty((R, _blocks(N)), dtype=_U8, device=dev)
+        _check(lib.situ_quant_fp8(dz.data_ptr(), 0, dq.data_ptr(), ds.data_ptr(), 1, R, N, 1, s))
         _check(lib.situ_linear_fp8_dgrad(dq.data_ptr(), ds.data_ptr(), wq.data_ptr(), ws.data_ptr(), off, E, da.data_ptr(),
                                          _ptr(status), R, N, K, s))
     if need_dw:
         dw = _empty((*lead, N, K), dtype=dw_dtype or _F32, device=dev)
         nb = lib.situ_linear_wgrad_workspace(R, N, K, E)
         buf = _scratch(nb, dout)
-        rows = situ_dequant_fp8(aq, as_)
+        rows = _empty((R, K), dtype=_BF16, device=dev)
+        _check(lib.situ_dequant_fp8(aq.data_ptr(), as_.data_ptr(), rows.data_ptr(), 0, 1, R, K, 1, s))
         _check(lib.situ_linear_wgrad(dz.data_ptr(), rows.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"), _ptr(buf), nb,
                                      _ptr(status), R, N, K, s))
     return da, dw, dbias
