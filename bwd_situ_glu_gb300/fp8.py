@@ -29,15 +29,18 @@ def _shape3(x, name):
     """(E, R, D) of a tensor [R, D] or [E, R, D] on a CUDA device."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dim() not in (2, 3) or not x.is_cuda:
-        raise ValueError(f"{name} must be a two- or three-dimensional CUDA tensor, got {tuple(x.shape)} on {x.device}")
-    return x.shape if x.dim() == 3 else (1, *x.shape)
+    shape = x.shape
+    n = len(shape)
+    if not (n == 2 or n == 3) or not x.is_cuda:
+        raise ValueError(f"{name} must be a two- or three-dimensional CUDA tensor, got {tuple(shape)} on {x.device}")
+    return shape if n == 3 else (1, *shape)
 
 
 def _scale_shape(shape, block_rows):
-    if block_rows not in (1, BLOCK):
+    if block_rows != 1 and block_rows != BLOCK:
         raise ValueError(f"block_rows must be 1 or {BLOCK}, got {block_rows!r}")
-    return (*shape[:-2], shape[-2] if block_rows == 1 else _blocks(shape[-2]), _blocks(shape[-1]))
+    *lead, R, D = shape
+    return (*lead, R if block_rows == 1 else (R + 127) // 128, (D + 127) // 128)
 
 
 def situ_quant_fp8(x, block_rows=1, codes=None, scales=None, stream=None):
@@ -45,15 +48,22 @@ def situ_quant_fp8(x, block_rows=1, codes=None, scales=None, stream=None):
     in blocks of 128 elements of a row (block_rows 1, the rows of a product) or 128 x 128 (128, a weight). A block's
     scale is the least power of two (2^-126 at least) with every finite value at most 448 times it; the code is
     x / scale rounded to nearest, ties to even, and 0x7F (NaN) for a value that is not finite."""
-    ty = _type(x, "x")
+    ty, dev = _type(x, "x"), x.device
+    shape = x.shape
     E, R, D = _shape3(x, "x")
-    dev, shape = x.device, tuple(x.shape)
-    _need(x, x.dtype, x.shape, dev, "x")
-    s_shape = _scale_shape(shape, block_rows)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, x, lambda: situ_quant_fp8(x, block_rows, codes, scales))
-    codes = _out(codes, shape, _U8, dev, "codes")
-    scales = _out(scales, s_shape, _U8, dev, "scales")
+    if codes is None:
+        codes = _empty(shape, dtype=_U8, device=dev)
+    else:
+        _need(codes, _U8, shape, dev, "codes")
+    s_shape = _scale_shape(shape, block_rows)
+    if scales is None:
+        scales = _empty(s_shape, dtype=_U8, device=dev)
+    else:
+        _need(scales, _U8, s_shape, dev, "scales")
     _check(_lib().situ_quant_fp8(x.data_ptr(), ty, codes.data_ptr(), scales.data_ptr(), E, R, D, block_rows,
                                  _raw_stream(dev.index)))
     return codes, scales
@@ -91,14 +101,22 @@ def _pair(t, name):
 def _weight(w, expert_offsets, dev):
     """(codes, scales, E, N, K, lead) of a quantised weight, [N,K] without expert_offsets, [E,N,K] with them."""
     wq, ws = _pair(w, "w")
-    if wq.dim() != (2 if expert_offsets is None else 3):
-        raise ValueError("w must be [N, K] without expert_offsets, [E, N, K] with them")
-    lead, (N, K) = tuple(wq.shape[:-2]), wq.shape[-2:]
-    E = lead[0] if lead else 1
-    _need(wq, _U8, (*lead, N, K), dev, "w codes")
-    _need(ws, _U8, (*lead, _blocks(N), _blocks(K)), dev, "w scales")
-    if expert_offsets is not None:
+    shape = wq.shape
+    if expert_offsets is None:
+        if len(shape) != 2:
+            raise ValueError("w must be [N, K] without expert_offsets, [E, N, K] with them")
+        E, lead = 1, ()
+        N, K = shape
+        s_shape = ((N + 127) // 128, (K + 127) // 128)
+    else:
+        if len(shape) != 3:
+            raise ValueError("w must be [N, K] without expert_offsets, [E, N, K] with them")
+        E, N, K = shape
+        lead = (E,)
+        s_shape = (E, (N + 127) // 128, (K + 127) // 128)
         _need(expert_offsets, _I64, (E + 1,), dev, "expert_offsets")
+    _need(wq, _U8, shape, dev, "w codes")
+    _need(ws, _U8, s_shape, dev, "w scales")
     return wq, ws, E, N, K, lead
 
 
