@@ -79,6 +79,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ uint16_t f32_to_bf16(float f) { return (uint16_t)(pack_bf16x2(f, 0.0f) & 0xFFFFu); }
 
+// Programmatic dependent launch. A kernel that lets its dependents go may still be at work when one of them begins;
+// dependents_wait, in a kernel launched with that attribute, returns when everything before it in the stream is done and visible (at
+// once without the attribute). Nothing that an earlier kernel may read or write is touched before it.
+__device__ __forceinline__ void let_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependents_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

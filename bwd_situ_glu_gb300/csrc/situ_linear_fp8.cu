@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int NT = (int)((NCOL + TILE - 1) / TILE);
     const int bbytes = block_bytes(most), sbytes = STAGE_KB * bbytes, stages = ring_stages(most);
 
-    build_plan(plan, offsets, E, R, most);
     if (threadIdx.x == 0) {                  // before pair_setup's fence and barriers
         for (int g = 0; g < GROUPS; ++g) {
             mbar_init(&sbars->full[g], 2);
@@ -150,6 +149,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     }
     const uint32_t tmem = pair_setup(bars, NUM_EPI_WARPS);
+    dependents_wait();
+    build_plan(plan, offsets, E, R, most);
+    __syncthreads();
     const int jobs = plan.start[E] * NT;
     const int j0 = blockIdx.x >> 1, jstep = gridDim.x >> 1;
 
@@ -459,6 +461,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
     __shared__ FewShared sh;
     __shared__ int tile_start[MAX_EXPERTS + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    dependents_wait();
     // first job of each expert: ceil(rows / FEW_ROWS) each
     if (threadIdx.x == 0) tile_start[0] = 0;
     const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) {
@@ -556,7 +559,7 @@ int launch_tc(const Args& p) {
     if (jobs > INT32_MAX - 2 * sms) return SITU_GLU_INVALID_ARG;     // the kernel counts them in 32 bits
     const int nb = (int)((p.N + QBLOCK - 1) / QBLOCK), kb = (int)((p.K + QBLOCK - 1) / QBLOCK);
     const ScaleStrides ss = {(int64_t)nb * kb, W_MN ? 1 : kb, W_MN ? kb : 1, W_MN ? kb : nb};
-    const cudaError_t e = launch_pairs(linear_fp8_tc_kernel<W_MN, ACT>, jobs, NUM_THREADS, SMEM_BYTES, p.stream, map_w, map_r, p.as,
+    const cudaError_t e = launch_pairs<true>(linear_fp8_tc_kernel<W_MN, ACT>, jobs, NUM_THREADS, SMEM_BYTES, p.stream, map_w, map_r, p.as,
                                        p.ws, ss, p.offsets, p.bias, (const uint16_t*)p.residual, p.out, p.out_fp32 ? 1 : 0,
                                        (uint16_t*)p.pre, p.status, (int)p.E, p.R, NCOL, (int)KB, most);
     return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
@@ -570,9 +573,17 @@ int launch_few(const Args& p) {
     const int64_t tiles = p.R < p.E ? p.R : (p.R + FEW_ROWS - 1) / FEW_ROWS + p.E;
     const int st = grid_for((const void*)kernel, FEW_WARPS * 32, tiles * ((p.N + 15) / 16) * FEW_WARPS, &grid);
     if (st != SITU_GLU_OK) return st;
-    kernel<<<grid, FEW_WARPS * 32, 0, p.stream>>>(p.a, p.as, p.w, p.ws, p.offsets, p.bias, (const uint16_t*)p.residual, p.out,
-                                                  p.out_fp32 ? 1 : 0, (uint16_t*)p.pre, (int)p.E, p.R, p.N, p.K);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(FEW_WARPS * 32);
+    cfg.stream = p.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p.a, p.as, p.w, p.ws, p.offsets, p.bias, (const uint16_t*)p.residual, p.out,
+                                             p.out_fp32 ? 1 : 0, (uint16_t*)p.pre, (int)p.E, p.R, p.N, p.K);
     return e == cudaSuccess ? SITU_GLU_OK : cuda_fail(e);
 }
 

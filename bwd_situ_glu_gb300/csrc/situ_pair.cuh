@@ -208,8 +208,9 @@ __device__ __forceinline__ void pair_drain(PairBars* bars, uint32_t pending, uin
         if (pending & (1u << s)) mbar_drain(&bars->full[s], (parity >> s) & 1u);
 }
 
-// Launch as clusters of 2, one CTA per SM, at most `pairs` clusters.
-template <class... KArgs, class... Args>
+// Launch as clusters of 2, one CTA per SM, at most `pairs` clusters; DEPENDENT: as a programmatic dependent launch, for a kernel that
+// calls dependents_wait.
+template <bool DEPENDENT = false, class... KArgs, class... Args>
 inline cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t pairs, int threads, int smem, cudaStream_t stream,
                                 Args... args) {
     int dev = 0, sms = 0;
@@ -220,7 +221,9 @@ inline cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t pairs, int thr
     if (pairs > sms / 2) pairs = sms / 2;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
@@ -230,7 +233,7 @@ inline cudaError_t launch_pairs(void (*kernel)(KArgs...), int64_t pairs, int thr
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = DEPENDENT ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

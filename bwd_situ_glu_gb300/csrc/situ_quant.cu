@@ -120,6 +120,7 @@ template <bool F32, int U, int TPB>
 __global__ void __launch_bounds__(TPB)
     quant_rows_kernel(const Chunk<F32>* __restrict__ x, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                       int64_t rows, int64_t cpr, int64_t nb, int64_t pieces) {
+    let_dependents_go();                     // a product usually follows: its launch and setup run beside this kernel's end
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (TPB / 32), items = rows * pieces;
     for (int64_t it = (int64_t)blockIdx.x * (TPB / 32) + (threadIdx.x >> 5); it < items; it += warps) {
@@ -157,6 +158,7 @@ template <bool F32>
 __global__ void __launch_bounds__(256)
     quant_rows_any_kernel(const void* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                           int64_t rows, int64_t D, int64_t nb) {
+    let_dependents_go();
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * 8, items = rows * nb;
     for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += warps) {

@@ -265,3 +265,34 @@ def test_refusals():
     with pytest.raises(sg.SituGluError) as err:
         lin((buf.view(torch.uint8).view(-1)[:128].view(4, 32), a[1]), w, out=buf)
     assert err.value.status == 2
+
+
+@pytest.mark.parametrize("R,N,K", [(3, 272, 4096), (700, 272, 4096), (4000, 80, 400)])
+def test_a_product_right_behind_its_quantiser(R, N, K):
+    """The product's launch overlaps the end of the kernel before it, whatever that is: the same buffers again and again, filled by a
+    copy and quantised in front of each product, the weights too; eagerly and replayed."""
+    w, xs = small_integers(N, K, seed=9), [small_integers(R, K, seed=i) for i in range(8)]
+    want = [(x.double() @ w.double().t()).to(BF) for x in xs]
+    x, codes, scales = torch.empty_like(xs[0]), *sg.situ_quant_fp8(xs[0])
+    wq = [t[0] for t in sg.situ_quant_fp8(w[None], block_rows=128)]
+    outs = [torch.empty(R, N, dtype=BF, device=DEV) for _ in xs]
+
+    def go():
+        for y, out in zip(xs, outs):
+            x.copy_(y)
+            sg.situ_quant_fp8(x, codes=codes, scales=scales)
+            sg.situ_quant_fp8(w, block_rows=128, codes=wq[0], scales=wq[1])
+            sg.situ_quant_fp8(x, codes=codes, scales=scales)
+            sg.situ_linear_fp8((codes, scales), wq, out=out)
+            sg.situ_linear_fp8((codes, scales), wq, out=out)
+    for _ in range(20):
+        go()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for out in outs:
+        out.zero_()
+    for _ in range(20):
+        graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
