@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from bwd_situ_glu_gb300 import _check, load as _lib, moe
-from bwd_situ_glu_gb300.moe import (_act, _device_now, _elsewhere, _empty, _need, _out, _ptr, _raw_stream, _scratch, _two, _type,
+from bwd_situ_glu_gb300.moe import (_act, _device_now, _elsewhere, _empty, _need, _out, _ptr, _raw_stream, _two, _type,
                                     _BF16, _CODE, _F32, _I32, _I64)
 
 _U8 = torch.uint8
@@ -23,6 +23,11 @@ BLOCK = 128   # elements of a row (or rows and columns of a weight) that share a
 
 def _blocks(n):
     return -(-n // BLOCK)
+
+
+def _up(n):
+    """Bytes up to a multiple of 256."""
+    return (n + 255) & -256
 
 
 def _shape3(x, name):
@@ -185,32 +190,33 @@ def situ_linear_fp8_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, d
         return _elsewhere(stream, dout, lambda: situ_linear_fp8_bwd(dout, a, w, expert_offsets, act, pre, dw_dtype, bias,
                                                                     need_da, need_dw, status))
     lib, s = _lib(), _raw_stream(dev.index)
+    off, codes, kept = _ptr(expert_offsets), R * N, R * N * 2 if code else 0
+    n_bias = lib.situ_linear_act_bwd_workspace(R, N, E) if bias else 0
+    n_dw = lib.situ_linear_wgrad_workspace(R, N, K, E) if need_dw else 0
+    # One buffer for what does not leave: dz behind an activation, and then in turn, in the stream's order, the bias sums'
+    # workspace, dz in 8 bits, and the decoded rows with the weight gradient's workspace. (A small step is all host time.)
+    first, rows_bytes = _up(kept), _up(R * K * 2)
+    buf = _empty(first + max(n_bias, _up(codes) + R * _blocks(N) if need_da else 0, rows_bytes + n_dw if need_dw else 0), dtype=_U8,
+                 device=dev)
+    base = buf.data_ptr()
+    at = base + first
+    dz = base if code else dout.data_ptr()
     da = dw = dbias = None
-    dz, off = dout, _ptr(expert_offsets)
     if code or bias:
-        if code:
-            dz = _empty((R, N), dtype=_BF16, device=dev)
-        nb, buf = 0, None
         if bias:
             dbias = _empty((*lead, N), dtype=_F32, device=dev)
-            nb = lib.situ_linear_act_bwd_workspace(R, N, E)
-            buf = _scratch(nb, dout)
-        _check(lib.situ_linear_act_bwd(dout.data_ptr(), _ptr(pre), code, off, E, dz.data_ptr() if code else 0,
-                                       _ptr(dbias), _ptr(buf), nb, R, N, s))
+        _check(lib.situ_linear_act_bwd(dout.data_ptr(), _ptr(pre), code, off, E, base if code else 0, _ptr(dbias), at if n_bias else 0,
+                                       n_bias, R, N, s))
     if need_da:
         da = _empty((R, K), dtype=_BF16, device=dev)
-        dq, ds = _empty((R, N), dtype=_U8, device=dev), _empty((R, _blocks(N)), dtype=_U8, device=dev)
-        _check(lib.situ_quant_fp8(dz.data_ptr(), 0, dq.data_ptr(), ds.data_ptr(), 1, R, N, 1, s))
-        _check(lib.situ_linear_fp8_dgrad(dq.data_ptr(), ds.data_ptr(), wq.data_ptr(), ws.data_ptr(), off, E, da.data_ptr(),
-                                         _ptr(status), R, N, K, s))
+        ds = at + _up(codes)
+        _check(lib.situ_quant_fp8(dz, 0, at, ds, 1, R, N, 1, s))
+        _check(lib.situ_linear_fp8_dgrad(at, ds, wq.data_ptr(), ws.data_ptr(), off, E, da.data_ptr(), _ptr(status), R, N, K, s))
     if need_dw:
         dw = _empty((*lead, N, K), dtype=dw_dtype or _F32, device=dev)
-        nb = lib.situ_linear_wgrad_workspace(R, N, K, E)
-        buf = _scratch(nb, dout)
-        rows = _empty((R, K), dtype=_BF16, device=dev)
-        _check(lib.situ_dequant_fp8(aq.data_ptr(), as_.data_ptr(), rows.data_ptr(), 0, 1, R, K, 1, s))
-        _check(lib.situ_linear_wgrad(dz.data_ptr(), rows.data_ptr(), off, E, dw.data_ptr(), _type(dw, "dw"), _ptr(buf), nb,
-                                     _ptr(status), R, N, K, s))
+        _check(lib.situ_dequant_fp8(aq.data_ptr(), as_.data_ptr(), at, 0, 1, R, K, 1, s))
+        _check(lib.situ_linear_wgrad(dz, at, off, E, dw.data_ptr(), _type(dw, "dw"), at + rows_bytes if n_dw else 0, n_dw, _ptr(status), R,
+                                     N, K, s))
     return da, dw, dbias
 
 
