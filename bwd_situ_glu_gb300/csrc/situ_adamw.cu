@@ -24,9 +24,10 @@ using namespace situ;
 using namespace situ_host;
 using namespace situ_fp8;
 
-// Instructions bound the step with states in 8 bits (some 85 an element: its IEEE root and quotient, the two codes, the random
-// bits), so what counts is how many warps an SM has to choose from and how often a block's setup is paid: 201M elements in
-// 128-thread blocks, 10 an SM, 8 passes, 534 us (0.90 of the copy rate); 256 threads and 4 passes 614, one pass 732.
+// Instructions bound the step with states in 8 bits (some 80 an element: its IEEE root and quotient, the two codes, the random
+// bits), so what counts is how many warps an SM has to choose from and how often a block's setup is paid: 201M elements, bf16
+// gradients and copies, in 128-thread blocks, 10 an SM, 8 passes, 519 us (0.93 of the copy rate; without paired products 534);
+// 8 or 12 blocks 552 / 535; 256 threads and 4 passes 600, one pass 732. States in fp32 run at the copy rate either way.
 constexpr int TPB = 128, BLOCKS_PER_SM = 10;
 constexpr int STEP = TPB * 8;                // elements of one pass of a block
 constexpr int PASSES = 8;
@@ -109,6 +110,17 @@ __device__ __forceinline__ int encode_moment(const float (&x)[8], const uint32_t
     return b;
 }
 
+__device__ __forceinline__ float2 two(const float (&x)[8], int k) { return make_float2(x[k], x[k + 1]); }
+// Products by the paired instruction, each half rounded as the single one; sums one by one: ptxas makes one operation of a paired
+// product and a paired sum, whatever rounding they ask for.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 both(float f) { return make_float2(f, f); }
+__device__ __forceinline__ void put(float (&x)[8], int k, float2 f) {
+    x[k] = f.x;
+    x[k + 1] = f.y;
+}
+
 template <bool BF16_GRAD, bool EIGHT, int CAP>
 __global__ void __launch_bounds__(TPB, BLOCKS_PER_SM)
     adamw_kernel(const __grid_constant__ Table<CAP> table, const Coefs given, const Coefs* __restrict__ from_device,
@@ -180,22 +192,25 @@ __global__ void __launch_bounds__(TPB, BLOCKS_PER_SM)
         if constexpr (EIGHT) {
             const float sm = live ? scale_value(t.ms[i0 / QBLOCK]) : 1.0f, sv = live ? scale_value(t.vs[i0 / QBLOCK]) : 1.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                m[k] = __fmul_rn(m[k], sm);
-                v[k] = __fmul_rn(v[k], sv);
-                v[k] = __fmul_rn(v[k], v[k]);
+            for (int k = 0; k < 8; k += 2) {
+                put(m, k, mul2(two(m, k), both(sm)));
+                const float2 root = mul2(two(v, k), both(sv));
+                put(v, k, mul2(root, root));
             }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (grad_scale) g[k] = __fmul_rn(g[k], gs);
-            const float m1 = __fadd_rn(__fmul_rn(c.b1, m[k]), __fmul_rn(c.c1, g[k]));
-            const float v1 = __fadd_rn(__fmul_rn(c.b2, v[k]), __fmul_rn(c.c2, __fmul_rn(g[k], g[k])));
-            const float root = __fsqrt_rn(v1);
-            const float q = __fadd_rn(__fmul_rn(root, c.r), c.eps);
-            w[k] = __fsub_rn(__fmul_rn(w[k], c.d), __fmul_rn(c.s, __fdiv_rn(m1, q)));
-            m[k] = m1;
-            v[k] = EIGHT ? root : v1;
+        for (int k = 0; k < 8; k += 2) {
+            float2 gk = two(g, k);
+            if (grad_scale) gk = mul2(gk, both(gs));
+            const float2 m1 = add2(mul2(both(c.b1), two(m, k)), mul2(both(c.c1), gk));
+            const float2 v1 = add2(mul2(both(c.b2), two(v, k)), mul2(both(c.c2), mul2(gk, gk)));
+            const float2 root = make_float2(__fsqrt_rn(v1.x), __fsqrt_rn(v1.y));
+            const float2 q = add2(mul2(root, both(c.r)), both(c.eps));
+            const float2 ratio = make_float2(__fdiv_rn(m1.x, q.x), __fdiv_rn(m1.y, q.y));
+            // w1 - s·ratio as w1 + (-s)·ratio: the same product but for its sign
+            put(w, k, add2(mul2(two(w, k), both(c.d)), mul2(both(-c.s), ratio)));
+            put(m, k, m1);
+            put(v, k, EIGHT ? root : v1);
         }
         if constexpr (EIGHT) {               // lanes without elements hold zeros and take part
             uint32_t r[8], qm[8], qv[8];
