@@ -8,11 +8,14 @@
 // What differs:
 //   * tcgen05.mma kind::mxf8f6f4 with block scales: the tensor core multiplies each 32-deep step of a row by a
 //     power of two held as a byte in TMEM, so the scales of 128-deep blocks cost neither instructions in the epilogue
-//     nor a rounding. A fifth role, the scale warp of each CTA, writes the bytes of four blocks at a time (its 128 weight
-//     rows': one byte for all; the chunk's rows': one each) in the layout that tcgen05.cp takes; the MMA warp copies a block's to
-//     TMEM in front of its four MMAs. Each byte stands four times in a word, once for each MMA of the block.
-//     (Handing over to the tensor core block by block, the proxy fence and the remote arrival, took longer than a
-//     block's products: 16385 x 3584 x 3584 in 380 us, four at a time 168, with the bytes fetched ahead 162.)
+//     nor a rounding. Two more warps of each CTA write the bytes of four blocks at a time (its 128 weight rows': one byte for
+//     all; the chunk's rows': one each) in the layout that tcgen05.cp takes; the MMA warp copies them to TMEM in front of
+//     the blocks' MMAs. Each byte stands four times in a word, once for each MMA of its block.
+//     The hand-over (fetch, shared memory, proxy fence, arrival at the leader) is what the speed hung on, 16385 x 3584 x 3584:
+//     block by block 380 us, four blocks at a time 168, the bytes fetched a turn ahead 160, two warps in turn 141, a group's copies
+//     at its start, so that its buffer is free again a group earlier, 133. Now bound by power: 1360 W at 1520 MHz in a long
+//     run (16384 rows 150 us, 2.8 PFLOP/s); at 1920 MHz a block of 224 rows takes 617 cycles with all pairs at work, 490 with 8, and
+//     448 are its products.
 //   * two accumulators and the scales share TMEM's 512 columns, so a chunk has at most 224 rows.
 //   * the dgrad reads W_e as stored (contraction apart, "MN-major"): boxes of 128 columns x 128 rows of bytes.
 //   * linear_fp8_few_kernel: for few rows per expert, as there.
@@ -54,9 +57,8 @@ constexpr int GROUP_KB = 4, GROUPS = SCALE_WARPS;   // blocks whose scales are h
 // TMEM holds the scales of GROUP_KB blocks; the tensor core takes copies and MMAs of one thread in order
 static_assert(SCALE_COL0 + GROUP_KB * 12 <= TMEM_COLS, "TMEM columns");
 
-// A ring stage: two blocks, of each 128 weight rows and half of the chunk's rows, 128 bytes each. (A stage's waits, its loads'
-// announcement and its commit take some 430 cycles however little it holds: with one block a stage 224 rows took 640
-// cycles a block.)
+// A ring stage: two blocks, of each 128 weight rows and half of the chunk's rows, 128 bytes each. (With 64 rows a block takes 404
+// cycles, in stages of one block 436; with 224 rows 620 either way.)
 constexpr int STAGE_KB = 2;
 __host__ __device__ constexpr int block_bytes(int most) { return PA_BYTES + most / 2 * KB8; }
 constexpr int RING_BYTES = 3 * STAGE_KB * block_bytes(MAX_CHUNK);
@@ -198,8 +200,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // ------------------------------------------------ MMA issuer (leader; the warp converged, one lane issues)
         // What this warp executes for a block is dependent instructions of one thread, and has to take less time than the
         // block's products (448 cycles for 224 rows): four blocks at a time with their offsets as constants, and a job's size
-        // from the scale warp. (With the scales' bookkeeping block by block and the work list searched here, a block took 670
-        // cycles with 64 rows and 750 with 224; 16385 x 3584 x 3584 160 us.)
+        // from the scale warps instead of the work list.
         if (rank == 0) {
             const bool elected = elect_one();
             int stage = 0, job = 0, group = 0;
