@@ -242,8 +242,12 @@ def _autograd():
             wq = situ_quant_fp8(w, block_rows=BLOCK) if wq is None else wq
             out = situ_linear_fp8(aq, wq, expert_offsets, bias, residual, act, save_pre=keep, status=status)
             out, pre = out if keep else (out, None)
-            if needs:          # the inputs only mark what the gradients depend on
-                ctx.save_for_backward(*aq, *wq, expert_offsets, pre, a if keep else None, w, bias if keep else None)
+            if needs:
+                # The last three only mark what the gradients depend on (a second derivative raises there). w does for a as well, where it
+                # has a gradient, and the rows need not be kept.
+                with_w = ctx.needs_input_grad[1]
+                ctx.save_for_backward(*(aq if with_w else (None, None)), *wq, expert_offsets, pre, a if keep and not with_w else None,
+                                      w if with_w else None, bias if keep else None)
             ctx.act, ctx.status, ctx.dw_dtype = act, status, w.dtype   # status is not saved as a tensor: the kernels write it
             return out
 
@@ -255,8 +259,8 @@ def _autograd():
                 return None, None, None, dout, *none
             aq, as_, wq, ws, expert_offsets, pre, a, w, bias = ctx.saved_tensors
             dout = dout.contiguous()
-            da, dw, db = situ_linear_fp8_bwd(dout, (aq, as_), (wq, ws), expert_offsets, ctx.act, pre, dw_dtype=ctx.dw_dtype,
-                                             bias=need[2], need_da=need[0], need_dw=need[1], status=ctx.status)
+            da, dw, db = situ_linear_fp8_bwd(dout, (aq, as_) if need[1] else None, (wq, ws), expert_offsets, ctx.act, pre,
+                                             dw_dtype=ctx.dw_dtype, bias=need[2], need_da=need[0], need_dw=need[1], status=ctx.status)
             da, dw, db = moe._once((da, dw, db), dout, a, w, bias)
             return da, dw, db, dout if need[3] else None, *none
 
@@ -268,7 +272,8 @@ def linear_fp8(a, w, bias=None, residual=None, expert_offsets=None, act="none", 
     """situ_linear_fp8 of bf16 rows a and a bf16 or fp32 weight w (both quantised here; ``wq``: w's codes and scales where
     the program has them, as after an optimizer step), bf16 out, differentiable in a, w (gradient in w's type), bias and
     residual. The gradients are those of the product of the quantised operands, taken for the operands' own (the codes'
-    rounding has no derivative). The backward keeps the rows' codes, not the rows."""
+    rounding has no derivative). The backward keeps the rows' codes, not the rows (those only where w has no gradient and an
+    activation follows), and ``wq`` itself: it has to stay as it is until then."""
     if wq is not None:
         if tuple(_pair(wq, "wq")[0].shape) != tuple(w.shape):
             raise ValueError("wq must be w's codes and scales")

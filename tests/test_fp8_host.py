@@ -61,8 +61,8 @@ def calls(monkeypatch):
         return (out, out.clone()) if save_pre else out
 
     def linear_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, dw_dtype=None, bias=True, need_da=True, need_dw=True, **kw):
-        made.append(("linear_bwd", dict(pre=pre is not None, bias=bias, need_da=need_da, need_dw=need_dw, dw_dtype=dw_dtype, w=w, **kw)))
-        return (torch.zeros(a[0].shape, dtype=BF) if need_da else None, torch.zeros(w[0].shape, dtype=dw_dtype) if need_dw else None,
+        made.append(("linear_bwd", dict(pre=pre is not None, a=a is not None, bias=bias, need_da=need_da, need_dw=need_dw, dw_dtype=dw_dtype, w=w, **kw)))
+        return (torch.zeros(dout.shape[0], w[0].shape[-1], dtype=BF) if need_da else None, torch.zeros(w[0].shape, dtype=dw_dtype) if need_dw else None,
                 torch.zeros(w[0].shape[:-1]) if bias else None)
 
     for name, f in dict(situ_quant_fp8=quant, situ_linear_fp8=linear, situ_linear_fp8_bwd=linear_bwd).items():
@@ -97,7 +97,7 @@ def test_what_the_backward_asks_for(calls, needed, act, dtype):
         asked = calls[3][1]
         assert len(calls) == 4 and asked["status"] is status and asked["dw_dtype"] is dtype
         assert (asked["need_da"], asked["need_dw"], asked["bias"]) == tuple(i in needed for i in range(3))
-        assert asked["pre"] is (act != "none")
+        assert asked["pre"] is (act != "none") and asked["a"] is (1 in needed)
     assert [t.grad is not None for t in ts] == [i in needed for i in range(4)]
     assert all(t.grad is None or t.grad.dtype == t.dtype for t in ts)
 
@@ -110,9 +110,18 @@ def test_given_codes_are_used_as_they_are(calls):
     assert all(torch.equal(x, y) for x, y in zip(calls[2][1]["w"], wq))
 
 
-def test_a_second_derivative_raises(calls):
-    ts = inputs(0, 1)
-    out = sg.fp8.linear_fp8(*ts)
-    (da,) = torch.autograd.grad(out.float().sum(), ts[0], create_graph=True)
+@pytest.mark.parametrize("needed,act", [((0, 1), "none"), ((0, 1), "gelu"), ((0,), "gelu"), ((1,), "none"), ((0, 2), "silu")])
+def test_a_second_derivative_raises(calls, needed, act):
+    """Whatever of the inputs a gradient depends on (without an activation a's is constant where w is)."""
+    ts = inputs(*needed)
+    first = ts[needed[0]]
+    (g,) = torch.autograd.grad(sg.fp8.linear_fp8(*ts, act=act).float().sum(), first, create_graph=True)
     with pytest.raises(RuntimeError, match="not\\s+differentiable"):
-        (da.float() * ts[1].float().sum()).sum().backward()
+        (g.float() * first.float()).sum().backward()
+
+
+def test_the_rows_themselves_are_not_kept(calls):
+    kept = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: kept.append(t.dtype) or t, lambda t: t):
+        out = sg.fp8.linear_fp8(*inputs(0, 1, 2, dtype=torch.float32), act="silu")
+    assert out.requires_grad and kept.count(BF) == 1         # the value before the activation
