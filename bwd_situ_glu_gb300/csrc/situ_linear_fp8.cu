@@ -263,62 +263,76 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     } else if (warp >= SCALE_WARP) {
         // ------------------------------------------------ scales (both CTAs): lane l has rows l, l + 32, .. of the chunk
-        // Each of the warps takes every SCALE_WARPS-th group of the pair's jobs, into a buffer of its own: some 300 dependent
-        // instructions, which took one warp longer than the products of the group's four blocks.
+        // Each of the warps takes every SCALE_WARPS-th group of the pair's jobs, into a buffer of its own: a turn takes one warp
+        // longer than the products of the group's four blocks. The order of a turn matters. The proxy fence waits for everything
+        // in flight, so the next group is fetched behind it (in front of it the fence took 1800 to 2900 cycles of the 4000 that
+        // two groups last); and finding the next job, some 1500 cycles with 112 experts, comes while those loads fly.
         const int group = warp - SCALE_WARP, NG = (KB + GROUP_KB - 1) / GROUP_KB;
         uint32_t phase = 0;
         const bool words = KB % 4 == 0 && (uintptr_t)row_scales % 4 == 0;
-        // A group's bytes, as loaded (a word of a row, or its bytes apart), a turn ahead: they are not touched before the next
-        // turn, which would wait for them here. 127 (a factor of 1) where there is nothing.
+        // A group's bytes, as loaded (a word of a row, or its bytes apart): they are not touched before the next turn, which would
+        // wait for them here. 127 (a factor of 1) where there is nothing.
         uint32_t raw_w[GROUP_KB], raw[7][GROUP_KB];
         auto fetch = [&](const Job& q, int kb) {
             const int cb = q.nt * 2 + rank;                      // this CTA's block of output columns
             const uint8_t* wp = w_scales + q.e * ws.per_expert + (int64_t)cb * ws.col_step + (int64_t)kb * ws.k_step;
             const uint8_t* rp = row_scales + (int64_t)(q.row0 + lane) * KB + kb;
+            const int left = cb < ws.col_blocks ? KB - kb : 0;
 #pragma unroll
             for (int k = 0; k < GROUP_KB; ++k) {
                 raw_w[k] = 127u;
-                if (cb < ws.col_blocks && kb + k < KB) raw_w[k] = __ldg(wp + (int64_t)k * ws.k_step);
+                if (k < left) raw_w[k] = __ldg(wp);
+                wp += ws.k_step;
             }
+            if (words) {
 #pragma unroll
-            for (int i = 0; i < 7; ++i) {
-                const bool live = lane + 32 * i < q.rows;
-                const uint8_t* p = rp + (int64_t)(32 * i) * KB;
-                raw[i][0] = 0x7F7F7F7Fu;
-                if (words) {
-                    if (live) raw[i][0] = __ldg((const uint32_t*)p);
-                } else {
+                for (int i = 0; i < 7; ++i) {
+                    raw[i][0] = 0x7F7F7F7Fu;
+                    if (lane + 32 * i < q.rows) raw[i][0] = __ldg((const uint32_t*)rp);
+                    rp += 32 * KB;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 7; ++i) {
 #pragma unroll
                     for (int k = 0; k < GROUP_KB; ++k) {
                         raw[i][k] = 127u;
-                        if (live && kb + k < KB) raw[i][k] = __ldg(p + k);
+                        if (lane + 32 * i < q.rows && kb + k < KB) raw[i][k] = __ldg(rp + k);
                     }
+                    rp += 32 * KB;
                 }
             }
         };
-        int j = j0, g = group;                                   // the next group: its job, and which of the job's
-        Job next = {};
-        auto settle = [&](bool moved) {                          // g may have run past its job's last
-            while (g >= NG) {
-                g -= NG;
-                j += jstep;
-                moved = true;
-            }
-            if (moved && j < jobs) next = job_at(j, plan, E, NT);
+        // Groups in order: one whose bytes are here, or on their way (job number, group of the job), and the one after it.
+        struct At {
+            int j, g;
+            Job q;
         };
-        settle(true);
-        if (j < jobs) fetch(next, g * GROUP_KB);
+        auto after = [&](const At& a) {
+            At b = a;
+            b.g += SCALE_WARPS;
+            while (b.g >= NG) {
+                b.g -= NG;
+                b.j += jstep;
+            }
+            if (b.j != a.j && b.j < jobs) b.q = job_at(b.j, plan, E, NT);
+            return b;
+        };
+        At next = {j0 - jstep, NG - SCALE_WARPS + group, Job{}};  // as if behind the job before the first
+        next = after(next);
+        At here = next;
+        if (here.j < jobs) {
+            fetch(here.q, here.g * GROUP_KB);
+            next = after(here);
+        }
         uint8_t* at = scales + group * GROUP_KB * SCALE_BYTES + lane * 16;
         const uint32_t full = cluster_addr(&sbars->full[group], 0);
-        while (j < jobs) {
-            const int blocks = min(GROUP_KB, KB - g * GROUP_KB), rows = next.n;
+        while (here.j < jobs) {
+            const int blocks = min(GROUP_KB, KB - here.g * GROUP_KB), rows = here.q.n;
             uint32_t b[7];
             const uint32_t wb = bytes4(raw_w[0], raw_w[1], raw_w[2], raw_w[3]);
 #pragma unroll
             for (int i = 0; i < 7; ++i) b[i] = words ? raw[i][0] : bytes4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]);
-            g += SCALE_WARPS;
-            settle(false);
-            if (j < jobs) fetch(next, g * GROUP_KB);
             uint32_t v[GROUP_KB][8];                             // before the wait: what follows it delays the products
 #pragma unroll
             for (int k = 0; k < GROUP_KB; ++k) {
@@ -339,6 +353,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(full);
             phase ^= 1;
+            here = next;
+            if (here.j < jobs) {
+                fetch(here.q, here.g * GROUP_KB);
+                next = after(here);
+            }
         }
     } else {
         linear_epilogue<ACT>(bars, plan, tmem, ACC_COLS, patches, bias, residual, out, out_fp32, pre, status, E, NCOL, NT, j0,
