@@ -13,9 +13,10 @@
 //     the blocks' MMAs. Each byte stands four times in a word, once for each MMA of its block.
 //     The hand-over (fetch, shared memory, proxy fence, arrival at the leader) is what the speed hung on, 16385 x 3584 x 3584:
 //     block by block 380 us, four blocks at a time 168, the bytes fetched a turn ahead 160, two warps in turn 141, a group's copies
-//     at its start, so that its buffer is free again a group earlier, 133. Now bound by power: 1360 W at 1520 MHz in a long
-//     run (16384 rows 150 us, 2.8 PFLOP/s); at 1920 MHz a block of 224 rows takes 617 cycles with all pairs at work, 490 with 8, and
-//     448 are its products.
+//     at its start, so that its buffer is free again a group earlier, 133. By %clock a block of 224 rows now takes 523 cycles,
+//     jobs' ends included, 448 of them its products (of 168 rows of ragged experts, weights from HBM: 615 of 336). What is
+//     left is power: the SMs run at 1.6 to 1.7 GHz in calls back to back, at 1.52 (1360 W) in a long run: 16384 rows 150 us,
+//     2.8 PFLOP/s.
 //   * two accumulators and the scales share TMEM's 512 columns, so a chunk has at most 224 rows.
 //   * the dgrad reads W_e as stored (contraction apart, "MN-major"): boxes of 128 columns x 128 rows of bytes.
 //   * linear_fp8_few_kernel: for few rows per expert, as there.
