@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import operator
+import threading
 
 import numpy as np
 import torch
@@ -62,7 +63,8 @@ class AdamWPlan:
     ``params``: fp32 tensors of any shape; ``m``, ``v``: fp32 of the same shapes, or uint8 codes with ``m_scales`` and
     ``v_scales`` (uint8, ceil(n / 128) each); ``work``: bf16 of the same shapes, or None. All contiguous, on one CUDA device, and
     no two sharing memory. The plan holds them; ``step`` updates them in place. A parameter's or working copy's ``.data`` may be
-    replaced between steps by one of the same kind; states are refilled with copy_ (a plan whose states were moved raises)."""
+    replaced between steps by one of the same kind; states are refilled with copy_ (a plan whose states were moved raises).
+    Steps from several threads are each taken whole."""
 
     def __init__(self, params, m, v, m_scales=None, v_scales=None, work=None):
         params, m, v = list(params), list(m), list(v)
@@ -95,6 +97,7 @@ class AdamWPlan:
                 self._table[:, column] = [t.data_ptr() for t in lists[name]]
         self._table[:, 7] = [p.numel() for p in params]
         self._table_ptr = self._table.ctypes.data
+        self._lock = threading.Lock()
         self._at = {name: [t.data_ptr() for t in ts] for name, ts in lists.items()}
 
     def _alike(self, tensors, dtype):
@@ -135,25 +138,26 @@ class AdamWPlan:
             raise ValueError("all tensors must be on the same device")
         if stream is not None or dev.index != _device_now():
             return _elsewhere(stream, self._params[0], lambda: self.step(grads, params, seed, grad_scale))
-        # A parameter's or working copy's .data may have been replaced since the last step, and is then checked again.
-        table = self._table
-        for name, at in self._at.items():
-            now = list(map(_T.data_ptr, self._lists[name]))
-            if now != at:
-                want, column = _MOVABLE.get(name, (None, None))
-                if want is None:
-                    raise ValueError(f"{name} is no longer where it was when the plan was made: make another plan")
-                for i, (p, shape) in enumerate(zip(self._lists[name], self._shapes)):
-                    _sg._need(p, want, shape, f"{name}[{i}]")
-                    if p.device != dev:
-                        raise ValueError("all tensors must be on the same device")
-                table[:, column] = self._at[name] = now
-        table[:, 1] = list(map(_T.data_ptr, grads))
         if not on_device and seed is None:
             seed = params.step
-        _check(_lib().situ_adamw_step(self._table_ptr, len(table), _CODE[kind], _E4M3 if self._eight else _CODE[_F32],
-                                      None if on_device else ctypes.byref(params), 0 if on_device else int(seed) & 0xFFFFFFFF,
-                                      params.data_ptr() if on_device else None, _ptr(grad_scale), _raw_stream(dev.index)))
+        with self._lock:                     # the table is read before the call returns, without Python's lock
+            table = self._table
+            # A parameter's or working copy's .data may have been replaced since the last step, and is then checked again.
+            for name, at in self._at.items():
+                now = list(map(_T.data_ptr, self._lists[name]))
+                if now != at:
+                    want, column = _MOVABLE.get(name, (None, None))
+                    if want is None:
+                        raise ValueError(f"{name} is no longer where it was when the plan was made: make another plan")
+                    for i, (p, shape) in enumerate(zip(self._lists[name], self._shapes)):
+                        _sg._need(p, want, shape, f"{name}[{i}]")
+                        if p.device != dev:
+                            raise ValueError("all tensors must be on the same device")
+                    table[:, column] = self._at[name] = now
+            table[:, 1] = list(map(_T.data_ptr, grads))
+            _check(_lib().situ_adamw_step(self._table_ptr, len(table), _CODE[kind], _E4M3 if self._eight else _CODE[_F32],
+                                          None if on_device else ctypes.byref(params), 0 if on_device else int(seed) & 0xFFFFFFFF,
+                                          params.data_ptr() if on_device else None, _ptr(grad_scale), _raw_stream(dev.index)))
 
 
 def situ_adamw_step(params, grads, m, v, hp, m_scales=None, v_scales=None, work=None, seed=None, grad_scale=None, stream=None):

@@ -4,6 +4,8 @@ With states in fp32 every stored value is one stated sequence of single IEEE fp3
 with states in 8 bits, whose rounding at random is a stated function of the seed and the element's place. The tests against
 64 bits count roundings: 2^-24 each, relative."""
 import ctypes
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -365,6 +367,39 @@ def test_another_stream_and_replaced_data():
     t["params"][0].data = t["params"][0].data[:69999].clone()
     with pytest.raises(ValueError):
         plan.step(t["grads"], hp)
+
+
+def test_steps_of_one_plan_from_two_threads(monkeypatch):
+    """The library reads a step's own gradients, however long it takes, while another thread steps the same plan."""
+    params = [torch.ones(64, device=DEV) for _ in range(3)]
+    plan = sg.AdamWPlan(params, **sg.adamw_state(params, "fp32"))
+    hp, seen, failed = sg.adam_params(step=1, **HP), [], []
+    grads = [[torch.full((64,), f, device=DEV) for _ in params] for f in (1.0, -3.0)]
+
+    class Slow:
+        def situ_adamw_step(self, table, count, *rest):
+            words = (ctypes.c_int64 * (8 * count)).from_address(table)
+            first = list(words)[1::8]
+            time.sleep(0.05)                             # without Python's lock, as the library's own call
+            seen.append((first, list(words)[1::8]))
+            return 0
+    monkeypatch.setattr(sg.adamw, "_lib", Slow)
+    start = threading.Barrier(2)
+
+    def run(gs):
+        try:
+            start.wait(60)
+            plan.step(gs, hp)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=run, args=(gs,)) for gs in grads]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    own = [[g.data_ptr() for g in gs] for gs in grads]
+    assert sorted(seen) == sorted((at, at) for at in own)
 
 
 def test_elements_past_32_bits():
