@@ -273,7 +273,9 @@ def linear_fp8(a, w, bias=None, residual=None, expert_offsets=None, act="none", 
     the program has them, as after an optimizer step), bf16 out, differentiable in a, w (gradient in w's type), bias and
     residual. The gradients are those of the product of the quantised operands, taken for the operands' own (the codes'
     rounding has no derivative). The backward keeps the rows' codes, not the rows (those only where w has no gradient and an
-    activation follows), and ``wq`` itself: it has to stay as it is until then."""
+    activation follows), and ``wq`` itself: it has to stay as it is until then. Before a backward is captured in a graph, every eager
+    graph of the same leaves has to be gone, as for any autograd operator: PyTorch ties a leaf's gradient to the stream that it was
+    first used on."""
     if wq is not None:
         if tuple(_pair(wq, "wq")[0].shape) != tuple(w.shape):
             raise ValueError("wq must be w's codes and scales")
