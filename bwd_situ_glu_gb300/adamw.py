@@ -20,7 +20,7 @@ import torch
 
 import bwd_situ_glu_gb300 as _sg
 from bwd_situ_glu_gb300 import AdamParams, _check, load as _lib
-from bwd_situ_glu_gb300.moe import _device_now, _elsewhere, _ptr, _raw_stream, _CODE, _F32, _BF16
+from bwd_situ_glu_gb300.moe import _device_now, _elsewhere, _increment_version, _ptr, _raw_stream, _CODE, _F32, _BF16
 
 _T, _U8 = torch.Tensor, torch.uint8
 _TYPES = {torch.Tensor, torch.nn.Parameter}
@@ -64,7 +64,9 @@ class AdamWPlan:
     ``v_scales`` (uint8, ceil(n / 128) each); ``work``: bf16 of the same shapes, or None. All contiguous, on one CUDA device, and
     no two sharing memory. The plan holds them; ``step`` updates them in place. A parameter's or working copy's ``.data`` may be
     replaced between steps by one of the same kind; states are refilled with copy_ (a plan whose states were moved raises).
-    Steps from several threads are each taken whole."""
+    Steps from several threads are each taken whole. To autograd a step is an operation in place on ``params`` and ``work``, as
+    PyTorch's optimizers are: a backward that has saved what one of them held before raises. (That goes by the tensors given here: pass
+    parameters, not their ``.data``. Replays of a captured step are not counted.)"""
 
     def __init__(self, params, m, v, m_scales=None, v_scales=None, work=None):
         params, m, v = list(params), list(m), list(v)
@@ -79,7 +81,7 @@ class AdamWPlan:
         for name, ts in lists.items():
             if len(ts) != len(params):
                 raise ValueError(f"{name} must have {len(params)} tensors, got {len(ts)}")
-        self._params, self._lists = params, lists
+        self._params, self._lists, self._updated = params, lists, params + lists.get("work", [])
         self._shapes = [p.shape for p in params if isinstance(p, torch.Tensor)]
         self._device = params[0].device if params and isinstance(params[0], torch.Tensor) else None
         state = _U8 if self._eight else _F32
@@ -158,6 +160,7 @@ class AdamWPlan:
             _check(_lib().situ_adamw_step(self._table_ptr, len(table), _CODE[kind], _E4M3 if self._eight else _CODE[_F32],
                                           None if on_device else ctypes.byref(params), 0 if on_device else int(seed) & 0xFFFFFFFF,
                                           params.data_ptr() if on_device else None, _ptr(grad_scale), _raw_stream(dev.index)))
+            _increment_version(self._updated)
 
 
 def situ_adamw_step(params, grads, m, v, hp, m_scales=None, v_scales=None, work=None, seed=None, grad_scale=None, stream=None):

@@ -7,14 +7,15 @@
 * ``linear_fp8``: the same as an autograd operator of bf16 rows and a bf16 or fp32 weight
 
 A quantised tensor is a pair (codes uint8, scale bytes uint8): a byte b stands for 2^(b-127). ``codes.view(torch.float8_e4m3fn)``
-are the codes' values. The conventions are those of the module ``moe``.
+are the codes' values. The conventions are those of the module ``moe``. Outputs that are given (``out``, ``codes``, ``scales``) count as
+written in place: a backward that has saved them raises.
 """
 from __future__ import annotations
 
 import torch
 
 from bwd_situ_glu_gb300 import _check, load as _lib, moe
-from bwd_situ_glu_gb300.moe import (_act, _device_now, _elsewhere, _empty, _need, _out, _ptr, _raw_stream, _two, _type,
+from bwd_situ_glu_gb300.moe import (_act, _device_now, _elsewhere, _empty, _need, _out, _ptr, _raw_stream, _two, _type, _written,
                                     _BF16, _CODE, _F32, _I32, _I64)
 
 _U8 = torch.uint8
@@ -60,6 +61,7 @@ def situ_quant_fp8(x, block_rows=1, codes=None, scales=None, stream=None):
         raise ValueError("x must be contiguous")
     if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, x, lambda: situ_quant_fp8(x, block_rows, codes, scales))
+    given = codes, scales
     if codes is None:
         codes = _empty(shape, dtype=_U8, device=dev)
     else:
@@ -71,6 +73,7 @@ def situ_quant_fp8(x, block_rows=1, codes=None, scales=None, stream=None):
         _need(scales, _U8, s_shape, dev, "scales")
     _check(_lib().situ_quant_fp8(x.data_ptr(), ty, codes.data_ptr(), scales.data_ptr(), E, R, D, block_rows,
                                  _raw_stream(dev.index)))
+    _written(*given)
     return codes, scales
 
 
@@ -88,9 +91,10 @@ def situ_dequant_fp8(codes, scales, block_rows=1, dtype=None, out=None, stream=N
         raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, codes, lambda: situ_dequant_fp8(codes, scales, block_rows, dtype, out))
-    out = _out(out, shape, dtype, dev, "out")
+    given, out = out, _out(out, shape, dtype, dev, "out")
     _check(_lib().situ_dequant_fp8(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), _CODE[dtype], E, R, D, block_rows,
                                    _raw_stream(dev.index)))
+    _written(given)
     return out
 
 
@@ -152,13 +156,14 @@ def situ_linear_fp8(a, w, expert_offsets=None, bias=None, residual=None, act="no
                                                               out_dtype, status))
     if out is not None:
         out_dtype = out.dtype
-    out = _out(out, (R, N), out_dtype or _BF16, dev, "out")
+    given, out = out, _out(out, (R, N), out_dtype or _BF16, dev, "out")
     if plain:
         aq, as_ = situ_quant_fp8(a)
     pre = _empty((R, N), dtype=_BF16, device=dev) if save_pre else None
     _check(_lib().situ_linear_fp8_fwd(aq.data_ptr(), as_.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(expert_offsets), E,
                                       _ptr(bias), _ptr(residual), code, out.data_ptr(), _type(out, "out"), _ptr(pre),
                                       _ptr(status), R, N, K, _raw_stream(dev.index)))
+    _written(given)
     return (out, pre) if save_pre else out
 
 
@@ -243,11 +248,12 @@ def _autograd():
             out = situ_linear_fp8(aq, wq, expert_offsets, bias, residual, act, save_pre=keep, status=status)
             out, pre = out if keep else (out, None)
             if needs:
-                # The last three only mark what the gradients depend on (a second derivative raises there). w does for a as well, where it
-                # has a gradient, and the rows need not be kept.
+                # a, w and bias only mark what the gradients depend on (a second derivative raises there). w does for a as well, where it
+                # has a gradient, and the rows need not be kept. Masters are not saved as tensors: the backward does not read them,
+                # and an optimizer may have written them before it.
                 with_w = ctx.needs_input_grad[1]
-                ctx.save_for_backward(*(aq if with_w else (None, None)), *wq, expert_offsets, pre, a if keep and not with_w else None,
-                                      w if with_w else None, bias if keep else None)
+                ctx.save_for_backward(*(aq if with_w else (None, None)), *wq, expert_offsets, pre, a if keep and not with_w else None)
+                ctx.masters = w if with_w else None, bias if keep else None
             ctx.act, ctx.status, ctx.dw_dtype = act, status, w.dtype   # status is not saved as a tensor: the kernels write it
             return out
 
@@ -257,11 +263,11 @@ def _autograd():
             none = (None,) * 5
             if not any(need[:3]):      # the residual's alone
                 return None, None, None, dout, *none
-            aq, as_, wq, ws, expert_offsets, pre, a, w, bias = ctx.saved_tensors
+            aq, as_, wq, ws, expert_offsets, pre, a = ctx.saved_tensors
             dout = dout.contiguous()
             da, dw, db = situ_linear_fp8_bwd(dout, (aq, as_) if need[1] else None, (wq, ws), expert_offsets, ctx.act, pre,
                                              dw_dtype=ctx.dw_dtype, bias=need[2], need_da=need[0], need_dw=need[1], status=ctx.status)
-            da, dw, db = moe._once((da, dw, db), dout, a, w, bias)
+            da, dw, db = moe._once((da, dw, db), dout, a, *ctx.masters)
             return da, dw, db, dout if need[3] else None, *none
 
     _function = LinearFp8
@@ -273,7 +279,7 @@ def linear_fp8(a, w, bias=None, residual=None, expert_offsets=None, act="none", 
     the program has them, as after an optimizer step), bf16 out, differentiable in a, w (gradient in w's type), bias and
     residual. The gradients are those of the product of the quantised operands, taken for the operands' own (the codes'
     rounding has no derivative). The backward keeps the rows' codes, not the rows (those only where w has no gradient and an
-    activation follows), and ``wq`` itself: it has to stay as it is until then. Before a backward is captured in a graph, every eager
+    activation follows), and ``wq`` itself: it has to stay as it is until then, or the backward raises (w and bias may be stepped before it). Before a backward is captured in a graph, every eager
     graph of the same leaves has to be gone, as for any autograd operator: PyTorch ties a leaf's gradient to the stream that it was
     first used on."""
     if wq is not None:

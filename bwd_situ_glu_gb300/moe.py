@@ -26,6 +26,7 @@ _T, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch
 _CODE = {_BF16: 0, _F32: 1}  # SITU_BF16, SITU_FP32
 _empty = torch.empty
 _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_increment_version = torch.autograd.graph.increment_version
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 MAX_EXPERTS, MAX_TOPK = 1024, 32  # SITU_MAX_EXPERTS, SITU_MAX_TOPK
@@ -78,6 +79,14 @@ def _out(t, shape, dtype, dev, name):
         return _empty(shape, dtype=dtype, device=dev)
     _need(t, dtype, shape, dev, name)
     return t
+
+
+def _written(*tensors):
+    """Tell autograd that a kernel wrote these (None: it allocated that output): a backward that still needs what they held raises then,
+    as behind PyTorch's own operators in place."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        _increment_version(given)
 
 
 def _scratch(nbytes, like):
@@ -412,20 +421,22 @@ def _autograd():
             keep = act != "none" and grad and any(ctx.needs_input_grad[:3])
             out = situ_linear(a, w, expert_offsets, bias, residual, act, save_pre=keep, status=status)
             out, pre = out if keep else (out, None)
-            ctx.save_for_backward(a, w, expert_offsets, pre, bias if keep else None)
-            ctx.act, ctx.status = act, status   # not saved as a tensor: the kernels write it
+            ctx.save_for_backward(a, w, expert_offsets, pre)
+            # not saved as tensors: the kernels write the status, and bias only marks what dz depends on (an optimizer may have written it
+            # before the backward, which does not read it)
+            ctx.act, ctx.status, ctx.bias = act, status, bias if keep else None
             return out
 
         @staticmethod
         def backward(ctx, dout):
-            a, w, expert_offsets, pre, bias = ctx.saved_tensors
+            a, w, expert_offsets, pre = ctx.saved_tensors
             need = ctx.needs_input_grad
             if not any(need[:3]):      # the residual's alone: no pre was kept
                 return None, None, None, dout, None, None, None, None
             dout = dout.contiguous()
             da, dw, db = situ_linear_bwd(dout, a, w, expert_offsets, ctx.act, pre, dw_dtype=_BF16,
                                          bias=need[2], need_da=need[0], need_dw=need[1], status=ctx.status)
-            da, dw, db = once((da, dw, db), dout, a, w, bias)
+            da, dw, db = once((da, dw, db), dout, a, w, ctx.bias)
             return da, dw, db, dout if need[3] else None, None, None, None, None
 
     _once = once
