@@ -24,7 +24,7 @@ from bwd_situ_glu_gb300.moe import _device_now, _elsewhere, _increment_version, 
 
 _T, _U8 = torch.Tensor, torch.uint8
 _TYPES = {torch.Tensor, torch.nn.Parameter}
-_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_dtype, _shape, _nbytes = operator.attrgetter("dtype"), operator.attrgetter("shape"), operator.attrgetter("nbytes")
 _E4M3 = 2         # SITU_E4M3
 _MOVABLE = {"params": (_F32, 0), "work": (_BF16, 6)}   # type and column of what may move between steps
 _COEFFICIENTS = 9  # words of situ_adamw_coefficients
@@ -63,7 +63,8 @@ class AdamWPlan:
     ``params``: fp32 tensors of any shape; ``m``, ``v``: fp32 of the same shapes, or uint8 codes with ``m_scales`` and
     ``v_scales`` (uint8, ceil(n / 128) each); ``work``: bf16 of the same shapes, or None. All contiguous, on one CUDA device, and
     no two sharing memory. The plan holds them; ``step`` updates them in place. A parameter's or working copy's ``.data`` may be
-    replaced between steps by one of the same kind; states are refilled with copy_ (a plan whose states were moved raises).
+    replaced between steps by one of the same kind; states are refilled with copy_ (a plan whose states were moved raises, and their
+    memory stays with the plan).
     Steps from several threads are each taken whole. To autograd a step is an operation in place on ``params`` and ``work``, as
     PyTorch's optimizers are: a backward that has saved what one of them held before raises. (That goes by the tensors given here: pass
     parameters, not their ``.data``. Replays of a captured step are not counted.)"""
@@ -101,6 +102,10 @@ class AdamWPlan:
         self._table_ptr = self._table.ctypes.data
         self._lock = threading.Lock()
         self._at = {name: [t.data_ptr() for t in ts] for name, ts in lists.items()}
+        # The place says that nothing moved only with what is there: of parameters and working copies the bytes are looked at again every
+        # step, and that they are contiguous; the states' memory cannot become another tensor's, for it is held here.
+        self._bytes = {name: [t.nbytes for t in lists[name]] for name in _MOVABLE if name in lists}
+        self._kept = [t.detach() for name, ts in lists.items() if name not in _MOVABLE for t in ts]
 
     def _alike(self, tensors, dtype):
         """Whether every one is contiguous, of this type, of its parameter's shape and on the plan's device: one pass of map for each
@@ -146,12 +151,13 @@ class AdamWPlan:
             table = self._table
             # A parameter's or working copy's .data may have been replaced since the last step, and is then checked again.
             for name, at in self._at.items():
-                now = list(map(_T.data_ptr, self._lists[name]))
-                if now != at:
-                    want, column = _MOVABLE.get(name, (None, None))
-                    if want is None:
-                        raise ValueError(f"{name} is no longer where it was when the plan was made: make another plan")
-                    for i, (p, shape) in enumerate(zip(self._lists[name], self._shapes)):
+                tensors = self._lists[name]
+                now = list(map(_T.data_ptr, tensors))
+                want, column = _MOVABLE.get(name, (None, None))
+                if now != at and want is None:
+                    raise ValueError(f"{name} is no longer where it was when the plan was made: make another plan")
+                if want and (now != at or list(map(_nbytes, tensors)) != self._bytes[name] or not all(map(_T.is_contiguous, tensors))):
+                    for i, (p, shape) in enumerate(zip(tensors, self._shapes)):
                         _sg._need(p, want, shape, f"{name}[{i}]")
                         if p.device != dev:
                             raise ValueError("all tensors must be on the same device")

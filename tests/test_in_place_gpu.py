@@ -70,3 +70,44 @@ def test_tensors_of_inference_mode():
         sg.situ_quant_fp8(x, codes=codes, scales=scales)
     plan.step([randn(300, seed=1)], sg.adam_params(step=2))
     assert torch.equal(sg.situ_dequant_fp8(codes, scales, out=torch.empty(4, 128, device=DEV)), sg.situ_dequant_fp8(codes, scales, dtype=torch.float32))
+
+
+# ---------------------------------------------------------------- a plan's tensors changed under it
+
+def test_data_at_the_same_place():
+    """A transposed square, a narrower view and memory that came back for a smaller tensor begin where the plan's tensor did: all are
+    refused, and nothing is written."""
+    p = [torch.zeros(64, 64, device=DEV), torch.zeros(2 ** 22, device=DEV)]
+    work = [t.to(BF) for t in p]
+    plan = sg.AdamWPlan(p, work=work, **sg.adamw_state(p))
+    g, hp = [torch.ones_like(t) for t in p], sg.adam_params(step=1)
+    for t in (p[0], work[0]):
+        t.data = t.data.t()
+        with pytest.raises(ValueError, match="contiguous"):
+            plan.step(g, hp)
+        t.data = t.data.t()
+    for t in (p[1], work[1]):
+        whole = t.data
+        t.data = whole[:1000]
+        with pytest.raises(ValueError, match="shape"):
+            plan.step(g, hp)
+        t.data = whole
+    assert not any(t.any() for t in (*p, *work))
+    plan.step(g, hp)
+    assert all((t != 0).all() for t in (*p, *work))
+
+
+@pytest.mark.parametrize("name", ["m", "v", "m_scales", "v_scales"])
+def test_states_given_up_by_the_program_stay_the_plans(name):
+    """A state whose tensor shrank in its place: the plan goes on with the memory that it was made with."""
+    plans = []
+    for shrink in (False, True):
+        p = [torch.zeros(5000, device=DEV)]
+        state = sg.adamw_state(p)
+        plan = sg.AdamWPlan(p, **state)
+        for k in (1, 2):
+            if shrink and k == 2:
+                state[name][0].data = state[name][0].data[:10]
+            plan.step([randn(5000, seed=k)], sg.adam_params(step=k))
+        plans.append((p[0], *plan._kept))
+    assert all(torch.equal(a, b) for a, b in zip(*plans))

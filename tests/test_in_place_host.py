@@ -1,7 +1,5 @@
 """What the bindings of the 8-bit operators and of AdamW tell autograd of tensors that their kernels write, and when a plan takes a
 tensor for what it was: without a GPU, the library replaced by one that notes its calls."""
-from types import SimpleNamespace
-
 import pytest
 import torch
 
@@ -52,9 +50,17 @@ def library(monkeypatch):
     return lib
 
 
+class Host:
+    """The host as a plan's device: its index is what get_device says of a tensor there."""
+    index = -1
+
+    def __eq__(self, other):
+        return other == torch.device("cpu")
+
+
 def plan_of(params, work=None, state="fp8"):
     plan = sg.AdamWPlan(params, work=work, **sg.adamw_state(params, state))
-    plan._device = SimpleNamespace(index=-1)             # what get_device says of a tensor on the host
+    plan._device = Host()
     return plan
 
 
@@ -154,3 +160,47 @@ def test_a_bias_may_be_stepped_before_the_backward_of_linear(library, step, monk
     step(plan_of([bias]))
     y.float().sum().backward()
     assert bias.grad is not None
+
+
+# ---------------------------------------------------------------- a plan's tensors changed under it
+
+def test_transposed_data_at_the_same_place(library, step):
+    """A square parameter, or working copy, whose .data became its transpose begins where it did, and pairs with other gradients."""
+    for which in ("params", "work"):
+        p = [torch.zeros(2, 2), torch.zeros(3, 3)]
+        plan = plan_of(p, [t.to(BF) for t in p])
+        t = plan._lists[which][1]
+        t.data = t.data.t()
+        with pytest.raises(ValueError, match="contiguous"):
+            step(plan)
+        t.data = t.data.t()
+        step(plan)
+        assert library.called.count("situ_adamw_step") == 1
+        library.called.clear()
+
+
+@pytest.mark.parametrize("which", ["params", "work"])
+def test_smaller_data_at_the_same_place(library, step, which):
+    """As where the old memory was released and came back for a smaller tensor: a step would write past its end."""
+    p = [torch.zeros(300), torch.zeros(40)]
+    plan = plan_of(p, [t.to(BF) for t in p])
+    t = plan._lists[which][0]
+    at = t.data_ptr()
+    t.data = t.data[:200]
+    assert t.data_ptr() == at
+    with pytest.raises(ValueError):
+        plan.step([torch.ones(300), torch.ones(40)], sg.adam_params(step=1))
+    assert "situ_adamw_step" not in library.called
+
+
+@pytest.mark.parametrize("state", ["fp32", "fp8"])
+def test_the_states_memory_is_the_plans(library, step, state):
+    """States are not looked at but for their place: their memory stays, whatever becomes of the tensors that were given."""
+    p = [torch.zeros(100000)]
+    plan = plan_of(p, state=state)
+    for name in set(plan._lists) - {"params"}:
+        t = plan._lists[name][0]
+        n, storage = t.untyped_storage().nbytes(), t.untyped_storage()._cdata
+        t.data = t.data[:1]                              # the same place
+        assert any(k.untyped_storage()._cdata == storage and k.untyped_storage().nbytes() == n for k in plan._kept)
+    step(plan)
