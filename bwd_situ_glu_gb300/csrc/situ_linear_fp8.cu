@@ -369,13 +369,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // ---------------------------------------------------------------- few rows per expert
 
-// A decoding step: the read of the weights is the whole cost. As linear_few_kernel: a job is 16 weight rows and up to
-// FEW_ROWS rows of one expert, the warps of a block share the contraction in steps of 256 (two scale blocks), and
+// A decoding step: the read of the weights is the whole cost. A job is 16 weight rows and all rows of one expert, FEW_ROWS at
+// most (the launch takes no more rows in all; linear_few_kernel, which does, cuts an expert's into several jobs), the warps of a block share the contraction in steps of 256 (two scale blocks), and
 // the products run on mma.m16n8k16 with the codes as fp16, which holds every E4M3 number. A lane's 16-byte
 // loads of weights and of the row at the same place are the fragments of four steps, the contraction's order being
 // free within a block. A block's sum is multiplied by its scales as it is added to the fp32 total.
 constexpr int FEW_WARPS = 8;
-constexpr int FEW_ROWS = 16;                 // rows of one job: 1 or 2 tiles of 8
+constexpr int FEW_ROWS = 16;                 // 1 or 2 tiles of 8
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -480,32 +480,28 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
                           const uint16_t* __restrict__ residual, void* __restrict__ out, int out_fp32,
                           uint16_t* __restrict__ pre, int E, int64_t R, int64_t N, int64_t K) {
     __shared__ FewShared sh;
-    __shared__ int tile_start[MAX_EXPERTS + 1];
+    __shared__ int owners[MAX_EXPERTS + 1];  // experts with rows before e
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     dependents_wait();
-    // first job of each expert: ceil(rows / FEW_ROWS) each
-    if (threadIdx.x == 0) tile_start[0] = 0;
-    const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) {
-        tile_start[e + 1] = (int)((en - b + FEW_ROWS - 1) / FEW_ROWS);
-    });
-    if (!orderly) drop_overlapping(offsets, E, R, tile_start + 1, nullptr);
-    if (warp == 0) prefix_in_place(tile_start, E, lane);
+    if (threadIdx.x == 0) owners[0] = 0;
+    const bool orderly = each_expert(offsets, E, R, [&](int e, int64_t b, int64_t en) { owners[e + 1] = en > b ? 1 : 0; });
+    if (!orderly) drop_overlapping(offsets, E, R, owners + 1, nullptr);
+    if (warp == 0) prefix_in_place(owners, E, lane);
     __syncthreads();
-    const int T = tile_start[E];
+    const int T = owners[E];
     const int groups = (int)((N + 15) / 16), KB = (int)((K + KB8 - 1) / KB8), NB = (int)((N + QBLOCK - 1) / QBLOCK);
     const int64_t jobs = (int64_t)T * groups;
     for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
         const int t = (int)(j / groups);
         const int64_t n0 = (int64_t)(j - (int64_t)t * groups) * 16;
-        int lo = 0, hi = E - 1;              // last e with tile_start[e] <= t
+        int lo = 0, hi = E - 1;              // last e with owners[e] <= t
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+            if (owners[mid] <= t) lo = mid; else hi = mid - 1;
         }
-        int64_t b, en;
-        expert_range(offsets, lo, R, b, en);
-        const int64_t row0 = b + (int64_t)(t - tile_start[lo]) * FEW_ROWS;
-        const int rows = (int)min((int64_t)FEW_ROWS, en - row0);
+        int64_t row0, end;
+        expert_range(offsets, lo, R, row0, end);
+        const int rows = (int)(end - row0);
         const uint8_t* we = w + (int64_t)lo * N * K;
         const uint8_t* se = ws + ((int64_t)lo * NB + n0 / QBLOCK) * KB;
         if (rows <= 8) few_job<1>(sh, a, as, we, se, row0, rows, n0, N, K, KB);
@@ -537,6 +533,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, 3)
 // 14336 x 3584: 1 row 13.0 / 16.0. 112 experts of 3584 x 2048: 8 rows 18.2 / 13.9, 128 rows 126 / 83, 448 rows 202 / 128; 8
 // experts of 1024 x 1024: 8 rows 5.2 / 8.3.)
 constexpr int64_t FEW_MAX_ROWS = 16;
+static_assert(FEW_MAX_ROWS <= FEW_ROWS, "an expert's rows are one job");
 constexpr int64_t FEW_MAX_WEIGHTS = 52 << 20;
 
 struct Args {
@@ -589,10 +586,10 @@ int launch_tc(const Args& p) {
 template <int ACT>
 int launch_few(const Args& p) {
     auto kernel = linear_fp8_few_kernel<ACT>;
-    // one warp of work per row as grid_for counts it: every 16 weight rows of every possible job
+    // one warp of work per row as grid_for counts it: every 16 weight rows of every expert that may have rows
     int grid = 0;
-    const int64_t tiles = p.R < p.E ? p.R : (p.R + FEW_ROWS - 1) / FEW_ROWS + p.E;
-    const int st = grid_for((const void*)kernel, FEW_WARPS * 32, tiles * ((p.N + 15) / 16) * FEW_WARPS, &grid);
+    const int64_t experts = p.R < p.E ? p.R : p.E;
+    const int st = grid_for((const void*)kernel, FEW_WARPS * 32, experts * ((p.N + 15) / 16) * FEW_WARPS, &grid);
     if (st != SITU_GLU_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
