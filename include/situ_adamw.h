@@ -14,8 +14,13 @@
  * a tensor, as situ_quant_fp8 chooses it (situ_fp8.h), so v = (code·2^(b-127))². Of the two codes around a value the step takes
  * the upper one (in magnitude) with the probability of the value's place between them, in 2^-16: a moment that moves by
  * less than a code's step (v by 1 - beta2 of itself) still moves, on average by what it should. Rounded to nearest it would stay
- * where it is. (The mean kept is the root's: v gains at most (1 - beta2)/16·|g² - v| a step besides.) A root above 0 gets a code above 0 (m/0 would throw its weight off); a value that is not finite
- * gets 0x7F (NaN).
+ * where it is. A root above 0 gets a code above 0 (m/0 would throw its weight off); a value that is not finite gets 0x7F (NaN).
+ * What that makes of v. The mean kept is the root's, so v itself comes out high. Where the root's code is one of E4M3's normal numbers
+ * (2^-6·2^(b-127) or more), v gains up to (1 - beta2)/16·|g² - v| a step on average. In the long run its mean lies above that of states in
+ * fp32 by 0.4 % for a constant gradient, by 2.5 to 4.6 % for independent normal ones (beta2 0.95 to 0.999), by 3.5 to 7.2 % for normal ones
+ * in one step of ten and 0 between, and never by more than 2/15; one element's v scatters by 0.24 to 0.43 of it. Below, at codes k = 1 .. 7,
+ * the gain is up to (1 - beta2)/(2k)·|g² - v|, and code 1 is a floor: the root of an element that ever had a gradient stays at
+ * 2^-9·2^(b-127) or above, 2^-17.8 to 2^-16.8 of its block's largest, so that elements so small step less than with states in fp32.
  * The 16 bits are those of mix(i + key) for element i of its tensor (modulo 2^32): the lower half for m, the upper for
  * v; key = mix(seed·0x9E3779B1), and mix(x) is x ^= x>>16, x *= 0x9E3779B1, x ^= x>>15, x *= 0x6A09E667, x ^= x>>16. No result
  * depends on timing, on the order of the tensors or on how they are split over calls.
