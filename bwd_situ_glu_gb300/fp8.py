@@ -15,8 +15,8 @@ from __future__ import annotations
 import torch
 
 from bwd_situ_glu_gb300 import _check, load as _lib, moe
-from bwd_situ_glu_gb300.moe import (_act, _device_now, _elsewhere, _empty, _need, _out, _ptr, _raw_stream, _two, _type, _written,
-                                    _BF16, _CODE, _F32, _I32, _I64)
+from bwd_situ_glu_gb300.moe import (_act, _device_now, _elsewhere, _empty, _need, _out, _ptr, _increment_version, _raw_stream, _two,
+                                    _type, _BF16, _CODE, _F32, _I32, _I64)
 
 _U8 = torch.uint8
 BLOCK = 128   # elements of a row (or rows and columns of a weight) that share a scale
@@ -61,7 +61,7 @@ def situ_quant_fp8(x, block_rows=1, codes=None, scales=None, stream=None):
         raise ValueError("x must be contiguous")
     if stream is not None or dev.index != _device_now():
         return _elsewhere(stream, x, lambda: situ_quant_fp8(x, block_rows, codes, scales))
-    given = codes, scales
+    given = None if codes is None and scales is None else [t for t in (codes, scales) if t is not None]
     if codes is None:
         codes = _empty(shape, dtype=_U8, device=dev)
     else:
@@ -73,7 +73,8 @@ def situ_quant_fp8(x, block_rows=1, codes=None, scales=None, stream=None):
         _need(scales, _U8, s_shape, dev, "scales")
     _check(_lib().situ_quant_fp8(x.data_ptr(), ty, codes.data_ptr(), scales.data_ptr(), E, R, D, block_rows,
                                  _raw_stream(dev.index)))
-    _written(*given)
+    if given:
+        _increment_version(given)
     return codes, scales
 
 
@@ -94,7 +95,8 @@ def situ_dequant_fp8(codes, scales, block_rows=1, dtype=None, out=None, stream=N
     given, out = out, _out(out, shape, dtype, dev, "out")
     _check(_lib().situ_dequant_fp8(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), _CODE[dtype], E, R, D, block_rows,
                                    _raw_stream(dev.index)))
-    _written(given)
+    if given is not None:
+        _increment_version(given)
     return out
 
 
@@ -163,7 +165,8 @@ def situ_linear_fp8(a, w, expert_offsets=None, bias=None, residual=None, act="no
     _check(_lib().situ_linear_fp8_fwd(aq.data_ptr(), as_.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(expert_offsets), E,
                                       _ptr(bias), _ptr(residual), code, out.data_ptr(), _type(out, "out"), _ptr(pre),
                                       _ptr(status), R, N, K, _raw_stream(dev.index)))
-    _written(given)
+    if given is not None:
+        _increment_version(given)
     return (out, pre) if save_pre else out
 
 

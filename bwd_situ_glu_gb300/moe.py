@@ -26,6 +26,8 @@ _T, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch
 _CODE = {_BF16: 0, _F32: 1}  # SITU_BF16, SITU_FP32
 _empty = torch.empty
 _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# Tells autograd that a kernel wrote a given tensor: a backward that still needs what it held raises then, as behind PyTorch's own
+# operators in place.
 _increment_version = torch.autograd.graph.increment_version
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
@@ -79,14 +81,6 @@ def _out(t, shape, dtype, dev, name):
         return _empty(shape, dtype=dtype, device=dev)
     _need(t, dtype, shape, dev, name)
     return t
-
-
-def _written(*tensors):
-    """Tell autograd that a kernel wrote these (None: it allocated that output): a backward that still needs what they held raises then,
-    as behind PyTorch's own operators in place."""
-    given = [t for t in tensors if t is not None]
-    if given:
-        _increment_version(given)
 
 
 def _scratch(nbytes, like):
