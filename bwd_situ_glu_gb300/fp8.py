@@ -286,14 +286,8 @@ def linear_fp8(a, w, bias=None, residual=None, expert_offsets=None, act="none", 
     graph of the same leaves has to be gone, as for any autograd operator: PyTorch ties a leaf's gradient to the stream that it was
     first used on."""
     if wq is not None:
-        if not isinstance(w, torch.Tensor):
-            raise TypeError("w must be a torch.Tensor")
         if tuple(_pair(wq, "wq")[0].shape) != tuple(w.shape):
             raise ValueError("wq must be w's codes and scales")
-        if w.requires_grad and torch.is_grad_enabled():      # its gradient is made in its type and beside the rows
-            _type(w, "w")
-            if isinstance(a, torch.Tensor) and w.device != a.device:
-                raise ValueError("all tensors must be on the same device")
     if isinstance(a, torch.Tensor) and a.dtype != _BF16:
         raise TypeError(f"a must be torch.bfloat16, got {a.dtype}")
     return _autograd().apply(a, w, bias, residual, expert_offsets, act, wq, status, torch.is_grad_enabled())

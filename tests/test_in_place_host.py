@@ -204,22 +204,3 @@ def test_the_states_memory_is_the_plans(library, step, state):
         t.data = t.data[:1]                              # the same place
         assert any(k.untyped_storage()._cdata == storage and k.untyped_storage().nbytes() == n for k in plan._kept)
     step(plan)
-
-
-# ---------------------------------------------------------------- weights that the backward has no gradient for
-
-@pytest.mark.parametrize("w,error", [(torch.zeros(32, 16, dtype=torch.float16), TypeError), (torch.zeros(32, 16, dtype=torch.float64), TypeError),
-                                     (torch.zeros(32, 16, device="meta"), ValueError)], ids=["fp16", "fp64", "device"])
-def test_weights_without_a_gradient_are_refused_before_the_product(library, w, error):
-    """With given codes the weight itself is not read; its gradient, where it takes one, is written in its type and beside the rows. One
-    that takes none may be anything."""
-    a, wq = torch.zeros(4, 16, dtype=BF, requires_grad=True), (torch.zeros(32, 16, dtype=U8), torch.ones(1, 1, dtype=U8))
-    with pytest.raises(error):
-        sg.fp8.linear_fp8(a, w.clone().requires_grad_(), wq=wq)
-    assert not library.called
-    assert sg.fp8.linear_fp8(a, w, wq=wq).requires_grad
-    with torch.no_grad():
-        sg.fp8.linear_fp8(a, w.clone().requires_grad_(), wq=wq)
-    for bad in (None, wq):
-        with pytest.raises(TypeError):
-            sg.fp8.linear_fp8(a, bad, wq=wq)
