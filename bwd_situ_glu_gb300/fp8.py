@@ -185,6 +185,8 @@ def situ_linear_fp8_bwd(dout, a, w, expert_offsets=None, act="none", pre=None, d
         aq, as_ = _pair(a, "a")
         _need(aq, _U8, (R, K), dev, "a codes")
         _need(as_, _U8, (R, _blocks(K)), dev, "a scales")
+        if dw_dtype is not None and dw_dtype not in _CODE:       # w's own, from linear_fp8
+            raise TypeError(f"dw_dtype must be torch.bfloat16 or torch.float32, got {dw_dtype}")
     code = _act(act)
     if code:
         if pre is None:

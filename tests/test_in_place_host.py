@@ -204,3 +204,22 @@ def test_the_states_memory_is_the_plans(library, step, state):
         t.data = t.data[:1]                              # the same place
         assert any(k.untyped_storage()._cdata == storage and k.untyped_storage().nbytes() == n for k in plan._kept)
     step(plan)
+
+
+# ---------------------------------------------------------------- weights that the backward has no gradient for
+
+def test_a_type_without_weight_gradients_is_refused_before_any_kernel(library):
+    dout, a = torch.zeros(4, 32, dtype=BF), (torch.zeros(4, 16, dtype=U8), torch.ones(4, 1, dtype=U8))
+    w = torch.zeros(32, 16, dtype=U8), torch.ones(1, 1, dtype=U8)
+    for dtype in (torch.float16, torch.float64, U8):
+        with pytest.raises(TypeError, match="dw_dtype"):
+            sg.situ_linear_fp8_bwd(dout, a, w, dw_dtype=dtype)
+        assert not library.called
+    assert sg.situ_linear_fp8_bwd(dout, None, w, dw_dtype=torch.float16, need_dw=False)[1] is None
+    # through autograd: the forward reads the given codes alone, and is fine with any weight
+    x, master = torch.zeros(4, 16, dtype=BF, requires_grad=True), torch.zeros(32, 16, dtype=torch.float16, requires_grad=True)
+    y = sg.fp8.linear_fp8(x, master, wq=w)
+    library.called.clear()
+    with pytest.raises(TypeError, match="dw_dtype"):
+        y.backward(dout)
+    assert not library.called
