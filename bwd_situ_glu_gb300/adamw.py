@@ -171,5 +171,6 @@ class AdamWPlan:
 
 
 def situ_adamw_step(params, grads, m, v, hp, m_scales=None, v_scales=None, work=None, seed=None, grad_scale=None, stream=None):
-    """AdamWPlan(params, m, v, m_scales, v_scales, work).step(grads, hp, seed, grad_scale, stream), for a single step."""
+    """AdamWPlan(params, m, v, m_scales, v_scales, work).step(grads, hp, seed, grad_scale, stream), for a single step. Making the plan is most
+    of its host time: 64 tensors 0.34 ms with states in fp32 and 0.48 ms in 8 bits, against 0.08 and 0.09 of a kept plan's step."""
     AdamWPlan(params, m, v, m_scales, v_scales, work).step(grads, hp, seed, grad_scale, stream)

@@ -235,7 +235,8 @@ __device__ __forceinline__ void linear_epilogue(PairBars* bars, const Plan& plan
 
 // Most rows per job, max_chunk at most. A job of n rows takes a 128-byte-deep block (64 of bf16, 128 in 8 bits: twice the
 // products in the same time) in the larger of 2n cycles (tensor cores) and the time
-// its (256 + n)·64 bytes per SM need at ~50 bytes a cycle (measured), and jobs run in rounds over the pairs of
+// its (256 + n)·64 bytes per SM need at ~50 bytes a cycle (measured of the bf16 product; the 8-bit one has since come to 523 cycles at
+// n = 224, 59 bytes a cycle, where this says 614: chunks that large count for a sixth too much there), and jobs run in rounds over the pairs of
 // SMs: 256 rows for large shapes, less where that would leave pairs without a job or a round mostly empty. A ring
 // stage is sized for them: with weights streamed from HBM the loads in flight count (112 experts of ~292 rows: five
 // 32 KB stages 562 us, six 523).

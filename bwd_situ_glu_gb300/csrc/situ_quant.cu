@@ -3,7 +3,8 @@
 // A block's scale is the least power of two that brings its largest finite value to 448 or below. 448 is
 // 1.75·2^8, so its exponent follows from the bits of that value alone, and x·2^-e is exact: the code's rounding
 // (cvt.rn.satfinite.e4m3x2) is the only one. One read of x, one write of codes; HBM-bound: 65537 x 3584 bf16 rows 112 us (0.94
-// of the copy rate), weights of 56 x 3584 x 2048 from fp32 335 us (0.92), 16384 x 2048 back to bf16 16 us (0.94).
+// of the copy rate), from fp32 190 us (0.93), weights of 56 x 3584 x 2048 from fp32 335 us (0.92), from bf16 273 us (0.68), 16384 x 2048
+// back to bf16 16 us (0.94).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -352,6 +353,9 @@ int launch_quant(const void* x, uint8_t* codes, uint8_t* scales, int64_t E, int6
         };
         // Few elements: one step a warp, over as many SMs as there are (one step / U steps, us, bf16 rows of 3584: 8 rows 1.4 /
         // 2.2, 256 rows 1.9 / 2.3, 512 rows 2.5 / 2.6, 1024 rows 3.4 / 3.0, 16384 rows 34.5 / 26.2; fp32 the same way).
+        // Measured of rows that run together; where D is no multiple of 128 a warp's U steps end with its row, and short rows
+        // leave most of them empty: bf16 262144 x 144 85 us (0.20 of the copy rate; fp32, U = 2, 64 us), 1048576 x 16 308 us
+        // (0.03), 65537 x 1008 40 us (0.75).
         return rows * cpr <= FEW_CHUNKS ? go(quant_rows_kernel<F32, 1, ROWS_TPB>, 1) : go(quant_rows_kernel<F32, U, ROWS_TPB>, U);
     }
     const int64_t rb = (R + QBLOCK - 1) / QBLOCK, tiles = E * rb * nb;
